@@ -43,6 +43,11 @@
  *   kda_chunk_fwd_rank2     two erase/write sub-steps per token
  *   kda_chunk_bwd_rank2     every gradient of the rank-2 forward (fp32)
  *   kda_decode_step         one token per (sequence, head), state in place
+ *   kda_linattn_chunk_fwd   linear attention with one decay per head: whole sequences
+ *   kda_linattn_chunk_bwd   every gradient of that forward
+ *   kda_linattn_decode_step its step for one token per (sequence, head), state in place
+ *   kda_state_quantize, kda_state_dequantize
+ *                           fp32 states into an 8-bit cache and back
  *   *_workspace_size        bytes of the caller-owned workspace of each call
  *   kda_check_gates, kda_check_seqlens   device checks of the inputs' contracts
  *   kda_device_status       failures the kernels recorded on the device
@@ -130,6 +135,10 @@ enum kda_status {
 #define KDA_DEVICE_WAIT_TIMEOUT 1u  /* a bounded wait inside a kernel ran out (about 2 s) */
 #define KDA_DEVICE_SLOT_MISSING 2u  /* split form: a chunk slot not written by this call's
                                        preparation kernel */
+#define KDA_DEVICE_BAD_INDEX    4u  /* a row or slot index of the state cache was too large */
+
+/* 8-bit formats of the state cache. */
+enum kda_cache_format { KDA_CACHE_INT8 = 0, KDA_CACHE_E4M3 = 1 };
 
 /*
  * kda_chunk_fwd -- chunked-parallel forward over whole sequences.
@@ -337,6 +346,106 @@ int kda_decode_step(int variant, int gate_range, int dtype,
                     float *state, void *o, unsigned flags, void *stream);
 
 /*
+ * Linear attention with one decay per head.
+ *
+ *   S_t = a_t S_{t-1} + k_t v_t^T ,  a_t = e^{g_t} ,   o_t = S_t^T q_t
+ *
+ * the recurrence without the erase term, the decay one number for each token
+ * and head instead of one for each key channel.  No scaling (a caller wanting
+ * 1/sqrt(d_k) pre-scales q).
+ *   q, k   : [B,T,Hk,d_k]   v, o : [B,T,H,d_v]   (bf16 or fp32, `dtype`)
+ *            H is a multiple of Hk; value head h uses query and key head
+ *            h / (H / Hk)
+ *   g      : fp32 log-decays, [B,T,H] (g_per_token != 0) or [H], one for each
+ *            head (g_per_token = 0).  Contract: g <= 0; -infinity is a decay
+ *            of 0 (nothing of the state is kept).  Not checked unless
+ *            KDA_FLAG_VALIDATE_RANGE asks for it.  g and dg need 4-byte
+ *            alignment only.
+ *   states : fp32 [N,H,d_k,d_v]
+ * cu_seqlens, num_seqs, initial_state, final_state and chunk_states as for
+ * kda_chunk_fwd_ws (chunk_states: the state after every 64 tokens of a
+ * sequence and after its last one, at the chunk slots described there).
+ * Sizes: B >= 1, T >= 0, d_k and d_v in {16, 32, 64, 128}, B*T < 2^30.
+ * Flags: KDA_FLAG_VALIDATE_RANGE (g and cu_seqlens; waits for the outcome) and
+ * KDA_FLAG_FORCE_SCAN (token-by-token kernel).  o does not depend on tokens
+ * behind it nor on other sequences of the batch, whatever their values.
+ */
+
+/*
+ * kda_linattn_chunk_fwd -- whole sequences.  workspace: caller-owned, 16-byte
+ * aligned, kda_linattn_chunk_fwd_workspace_size(...) bytes (with the call's
+ * flags; 0: may be NULL), not read before it is written; two calls that may
+ * overlap on the GPU need one each.
+ */
+size_t kda_linattn_chunk_fwd_workspace_size(int dtype, int B, int T, int Hk, int H, int d_k, int d_v,
+                                            int has_cu_seqlens, int num_seqs, unsigned flags);
+int kda_linattn_chunk_fwd(int dtype, int B, int T, int Hk, int H, int d_k, int d_v,
+                          const void *q, const void *k, const void *v, const float *g, int g_per_token,
+                          const int32_t *cu_seqlens, int num_seqs, const float *initial_state,
+                          float *final_state, float *chunk_states, void *o, void *workspace,
+                          size_t workspace_bytes, unsigned flags, void *stream);
+
+/*
+ * kda_linattn_chunk_bwd -- its gradients, for L with dL/do = d_o [B,T,H,d_v]
+ * (the inputs' dtype) and dL/dS_final = d_final_state (NULL = 0): dq, dk, dv
+ * in the inputs' dtype and layouts (dq and dk summed over the value heads that
+ * share them), dg fp32 in g's layout (summed over all tokens for g of [H]),
+ * d_initial_state fp32 (NULL: not written).  Each is formed in fp32 and
+ * rounded once.  With G_t = dL/dS_t,
+ *   dq_t = S_t d_o_t,  dk_t = G_t v_t,  dv_t = G_t^T k_t,
+ *   G_t = a_{t+1} G_{t+1} + q_t d_o_t^T,
+ *   dg_t = sum_{r >= t} (q_r . dq_r - k_r . dk_r) + <S_T, dL/dS_T>.
+ * At g_t = -infinity dg_t is 0, the slope of e^g there.  Deterministic.  workspace as above, kda_linattn_chunk_bwd_workspace_size
+ * bytes.  Flags: KDA_FLAG_FORCE_SCAN.
+ */
+size_t kda_linattn_chunk_bwd_workspace_size(int dtype, int B, int T, int Hk, int H, int d_k, int d_v,
+                                            int has_cu_seqlens, int num_seqs);
+int kda_linattn_chunk_bwd(int dtype, int B, int T, int Hk, int H, int d_k, int d_v,
+                          const void *q, const void *k, const void *v, const float *g, int g_per_token,
+                          const int32_t *cu_seqlens, int num_seqs, const float *initial_state,
+                          const void *d_o, const float *d_final_state,
+                          void *dq, void *dk, void *dv, float *dg, float *d_initial_state,
+                          void *workspace, size_t workspace_bytes, unsigned flags, void *stream);
+
+/*
+ * kda_linattn_decode_step -- one step for N sequences: q, k [N,Hk,d_k]; v, o
+ * [N,H,d_v]; g [N,H] (g_per_token != 0) or [H]; state fp32 [N,H,d_k,d_v], read
+ * and overwritten in place.  Flags: KDA_FLAG_VALIDATE_RANGE.
+ */
+int kda_linattn_decode_step(int dtype, int N, int Hk, int H, int d_k, int d_v,
+                            const void *q, const void *k, const void *v, const float *g, int g_per_token,
+                            float *state, void *o, unsigned flags, void *stream);
+
+/*
+ * Quantised state cache: fp32 states (final states, chunk_states snapshots,
+ * decode states of any operator here) kept as 8-bit codes with one fp32 scale
+ * for each (slot, head, key channel).
+ *   codes  : [num_slots,H,d_k,d_v] int8 or e4m3 (`format`)
+ *   scales : [num_slots,H,d_k] fp32
+ * For a row x of d_v values with A = max |x|: scale = A / TOP, TOP = 127
+ * (int8) or 448 (e4m3); code = the nearest to x TOP / A, ties to the even
+ * code, decided as in exact arithmetic; the value read back is code * scale.
+ * A row of zeros has scale 0.  A row that holds a NaN or an infinity has scale
+ * NaN and reads back as NaN.
+ *
+ * kda_state_quantize   -- entry i (0 <= i < n) writes state rows[i] of
+ *   `states` [num_states,H,d_k,d_v] to slot slots[i].  rows, slots: int32
+ *   DEVICE arrays of n entries, NULL = 0 .. n-1.  An entry with a negative row
+ *   or slot is skipped; where several entries name one slot, the last one is
+ *   written.  Slots that no entry names are left as they are.
+ * kda_state_dequantize -- states[i] = slot slots[i], for `states`
+ *   [n,H,d_k,d_v]; a negative slot gives zeros (an empty state).
+ * An index that is too large is never followed: the entry is skipped (written
+ * as NaN by kda_state_dequantize) and KDA_DEVICE_BAD_INDEX is recorded for
+ * kda_device_status.
+ */
+int kda_state_quantize(int format, int n, int num_states, int num_slots, int H, int d_k, int d_v,
+                       const float *states, const int32_t *rows, const int32_t *slots, void *codes,
+                       float *scales, void *stream);
+int kda_state_dequantize(int format, int n, int num_slots, int H, int d_k, int d_v, const void *codes,
+                         const float *scales, const int32_t *slots, float *states, void *stream);
+
+/*
  * kda_check_gates -- count gates outside the declared range on the device.
  * Checks alpha [n_tok*d_k] against the range's alpha interval and g1 (beta/e,
  * n_tok values; GDN-2 b, n_tok*d_k values, against [0, 2] for the extended
@@ -369,8 +478,10 @@ int kda_check_seqlens(const int32_t *cu_seqlens, int num_seqs, long long total_t
  * attribute theirs.  Failures a kernel records: a bounded mbarrier wait that
  * ran out (about 2 s; only a broken pipeline gets near it; the kernel then
  * drains its copies in flight, writes NaN to the final state of its
- * (sequence, head) and exits), and in the split form a chunk slot that this
- * call's preparation kernel did not complete.  No kernel traps.
+ * (sequence, head) and exits), in the split form a chunk slot that this
+ * call's preparation kernel did not complete, and a state-cache index that was
+ * too large (KDA_DEVICE_BAD_INDEX; that entry alone is affected).  No kernel
+ * traps.
  */
 int kda_device_status(void *stream, unsigned *bits);
 

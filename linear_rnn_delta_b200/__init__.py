@@ -19,6 +19,8 @@ import torch
 
 __all__ = ["kda_chunk_fwd", "kda_chunk_bwd", "KdaChunkFunction", "kda_chunk_fwd_rank2", "kda_chunk_bwd_rank2",
            "kda_decode_step",
+           "kda_linattn_chunk_fwd", "kda_linattn_chunk_bwd", "KdaLinAttnFunction", "kda_linattn_decode_step",
+           "kda_state_quantize", "kda_state_dequantize", "CACHE_FORMATS", "DEVICE_BAD_INDEX",
            "kda_check_gates", "kda_check_seqlens", "kda_device_status", "kda_error_string", "kda_version",
            "KdaError", "VARIANTS", "RANGES", "LIB_PATH", "FLAG_VALIDATE_RANGE", "FLAG_FORCE_SCAN",
            "FLAG_FORCE_FUSED", "FLAG_FORCE_SPLIT", "FLAG_GATE_LOGITS", "FLAG_L2NORM_K", "FLAG_DEBUG_STALL",
@@ -38,6 +40,8 @@ FLAG_L2NORM_K = 32     # k given unnormalised; the kernels L2-normalise it per t
 FLAG_DEBUG_STALL = 64  # testing aid (with FLAG_FORCE_SPLIT): one chain CTA's first wait runs out
 DEVICE_WAIT_TIMEOUT = 1   # kda_device_status bits
 DEVICE_SLOT_MISSING = 2
+DEVICE_BAD_INDEX = 4      # a state-cache row or slot index was too large
+CACHE_FORMATS = {torch.int8: 0, torch.float8_e4m3fn: 1}
 
 _vp = ctypes.c_void_p
 _i = ctypes.c_int
@@ -51,7 +55,9 @@ def _load():
     for name in ("kda_chunk_fwd", "kda_chunk_fwd_ws", "kda_chunk_fwd_workspace_size", "kda_chunk_bwd",
                  "kda_chunk_bwd_workspace_size", "kda_chunk_fwd_rank2", "kda_chunk_fwd_rank2_workspace_size",
                  "kda_chunk_bwd_rank2", "kda_chunk_bwd_rank2_workspace_size",
-                 "kda_decode_step", "kda_check_gates", "kda_check_seqlens", "kda_device_status", "kda_error_string",
+                 "kda_decode_step", "kda_linattn_chunk_fwd", "kda_linattn_chunk_fwd_workspace_size",
+                 "kda_linattn_chunk_bwd", "kda_linattn_chunk_bwd_workspace_size", "kda_linattn_decode_step",
+                 "kda_state_quantize", "kda_state_dequantize", "kda_check_gates", "kda_check_seqlens", "kda_device_status", "kda_error_string",
                  "kda_last_error_detail", "kda_version"):
         if not hasattr(lib, name):
             raise ImportError(f"{LIB_PATH} lacks {name}: it is stale, rebuild it with "
@@ -79,6 +85,22 @@ def _load():
     lib.kda_chunk_bwd_rank2_workspace_size.argtypes = [_i] * 8
     lib.kda_decode_step.restype = _i
     lib.kda_decode_step.argtypes = [_i] * 7 + [_vp] * 6 + [_vp, _vp, ctypes.c_uint, _vp]
+    lib.kda_linattn_chunk_fwd.restype = _i
+    lib.kda_linattn_chunk_fwd.argtypes = ([_i] * 7 + [_vp] * 4 + [_i, _vp, _i] + [_vp] * 5 +
+                                          [ctypes.c_size_t, ctypes.c_uint, _vp])
+    lib.kda_linattn_chunk_fwd_workspace_size.restype = ctypes.c_size_t
+    lib.kda_linattn_chunk_fwd_workspace_size.argtypes = [_i] * 9 + [ctypes.c_uint]
+    lib.kda_linattn_chunk_bwd.restype = _i
+    lib.kda_linattn_chunk_bwd.argtypes = ([_i] * 7 + [_vp] * 4 + [_i, _vp, _i] + [_vp] * 9 +
+                                          [ctypes.c_size_t, ctypes.c_uint, _vp])
+    lib.kda_linattn_chunk_bwd_workspace_size.restype = ctypes.c_size_t
+    lib.kda_linattn_chunk_bwd_workspace_size.argtypes = [_i] * 9
+    lib.kda_linattn_decode_step.restype = _i
+    lib.kda_linattn_decode_step.argtypes = [_i] * 6 + [_vp] * 4 + [_i, _vp, _vp, ctypes.c_uint, _vp]
+    lib.kda_state_quantize.restype = _i
+    lib.kda_state_quantize.argtypes = [_i] * 7 + [_vp] * 6
+    lib.kda_state_dequantize.restype = _i
+    lib.kda_state_dequantize.argtypes = [_i] * 6 + [_vp] * 5
     lib.kda_check_gates.restype = _i
     lib.kda_check_gates.argtypes = [_i, _i, _i, ctypes.c_longlong, _i, _vp, _vp, _vp, _vp]
     lib.kda_check_seqlens.restype = _i
@@ -464,6 +486,229 @@ def kda_decode_step(variant: Union[str, int], gate_range: Union[str, int], q: to
     if rc != 0:
         raise KdaError(rc, "kda_decode_step")
     return o
+
+
+def _lin_inputs(q, k, v, g, packed):
+    """Shapes of linear attention's inputs ([B,T,heads,d], or [N,heads,d] for a decode step), checked."""
+    lead = 2 if packed else 1
+    if q.dim() != lead + 2 or v.dim() != lead + 2:
+        raise ValueError("q, k must be [B,T,Hk,d_k] and v [B,T,H,d_v]" if packed else
+                         "q, k must be [N,Hk,d_k] and v [N,H,d_v]")
+    dt, dev = q.dtype, q.device
+    if dt not in _DTYPES:
+        raise ValueError(f"dtype {dt} unsupported (bf16 or fp32)")
+    (Hk, dk), (H, dv) = q.shape[lead:], v.shape[lead:]
+    if Hk < 1 or H % Hk:
+        raise ValueError(f"{H} value heads are not a multiple of {Hk} query and key heads")
+    _check(q, "q", dt, q.shape, dev)
+    _check(k, "k", dt, q.shape, dev)
+    _check(v, "v", dt, (*q.shape[:lead], H, dv), dev)
+    per_token = g.dim() != 1
+    _check(g, "g", torch.float32, (*q.shape[:lead], H) if per_token else (H,), dev)
+    return dt, dev, Hk, H, dk, dv, int(per_token)
+
+
+def _num_seqs(cu_seqlens, B, dev):
+    if cu_seqlens is None:
+        return B
+    if cu_seqlens.dtype != torch.int32 or not cu_seqlens.is_cuda or cu_seqlens.dim() != 1:
+        raise ValueError("cu_seqlens must be a 1-D int32 CUDA tensor")
+    _check(cu_seqlens, "cu_seqlens", torch.int32, cu_seqlens.shape, dev)
+    return cu_seqlens.numel() - 1
+
+
+def _launching(stream, dev):
+    """Context in which a call allocates and launches: the tensors' device, and the memory pool of the stream
+    that the kernels run on (what torch hands out is then free on that stream)."""
+    if stream is None:
+        return torch.cuda.device(dev)
+    return torch.cuda.stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream), dev))
+
+
+def kda_linattn_chunk_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor,
+                          cu_seqlens: Optional[torch.Tensor] = None, initial_state: Optional[torch.Tensor] = None,
+                          final_state: Union[torch.Tensor, bool, None] = True, o: Optional[torch.Tensor] = None,
+                          flags: int = 0, stream=None, chunk_states: Union[torch.Tensor, bool, None] = None):
+    """Linear attention with one decay per head over whole sequences (C:
+    kda_linattn_chunk_fwd): S_t = e^{g_t} S_{t-1} + k_t v_t^T, o_t = S_t^T q_t.
+
+    q, k [B,T,Hk,d_k]; v [B,T,H,d_v], H a multiple of Hk (value head h uses
+    query and key head h // (H // Hk)); g fp32 log-decays (<= 0), [B,T,H] or
+    one for each head [H].  Other arguments and results as for kda_chunk_fwd:
+    returns (o, final_state or None), plus chunk_states when requested.
+    """
+    dt, dev, Hk, H, dk, dv, per_token = _lin_inputs(q, k, v, g, True)
+    B, T = q.shape[:2]
+    N = _num_seqs(cu_seqlens, B, dev)
+    f32 = dict(dtype=torch.float32, device=dev)
+    states, snaps = (N, H, dk, dv), (num_chunk_slots(B, T, N), H, dk, dv)
+    want_states = chunk_states is not None and chunk_states is not False
+    _check(initial_state, "initial_state", torch.float32, states, dev)
+    sizes = (_DTYPES[dt], B, T, Hk, H, dk, dv)
+    with _launching(stream, dev):
+        if final_state is True:
+            final_state = torch.empty(states, **f32)
+        elif final_state is False:
+            final_state = None
+        if chunk_states is True:
+            chunk_states = torch.empty(snaps, **f32)
+        elif chunk_states is False:
+            chunk_states = None
+        if o is None:
+            o = torch.empty((B, T, H, dv), dtype=dt, device=dev)
+        _check(final_state, "final_state", torch.float32, states, dev)
+        _check(o, "o", dt, (B, T, H, dv), dev)
+        _check(chunk_states, "chunk_states", torch.float32, snaps, dev)
+        ws_bytes = lib.kda_linattn_chunk_fwd_workspace_size(*sizes, int(cu_seqlens is not None), N, int(flags))
+        ws = torch.empty(ws_bytes, dtype=torch.uint8, device=dev) if ws_bytes else None
+        rc = lib.kda_linattn_chunk_fwd(*sizes, _ptr(q), _ptr(k), _ptr(v), _ptr(g), per_token, _ptr(cu_seqlens), N,
+                                       _ptr(initial_state), _ptr(final_state), _ptr(chunk_states), _ptr(o), _ptr(ws),
+                                       ws_bytes, int(flags), _stream(stream, dev))
+    if rc != 0:
+        raise KdaError(rc, "kda_linattn_chunk_fwd")
+    if want_states:
+        return o, final_state, chunk_states
+    return o, final_state
+
+
+def kda_linattn_chunk_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor, d_o: torch.Tensor,
+                          d_final_state: Optional[torch.Tensor] = None, cu_seqlens: Optional[torch.Tensor] = None,
+                          initial_state: Optional[torch.Tensor] = None, d_initial_state: bool = True,
+                          flags: int = 0, stream=None):
+    """Gradients of kda_linattn_chunk_fwd (C: kda_linattn_chunk_bwd) for a loss
+    with dL/do = d_o ([B,T,H,d_v], the inputs' dtype) and dL/dS_final =
+    d_final_state (fp32 or None for zero).  Returns (dq, dk, dv, dg,
+    d_initial_state): dq, dk, dv in the inputs' dtype (dq and dk summed over
+    the value heads that share them), dg fp32 shaped like g, d_initial_state
+    fp32 (None unless ``d_initial_state``)."""
+    dt, dev, Hk, H, dk, dv, per_token = _lin_inputs(q, k, v, g, True)
+    B, T = q.shape[:2]
+    _check(d_o, "d_o", dt, v.shape, dev)
+    N = _num_seqs(cu_seqlens, B, dev)
+    _check(initial_state, "initial_state", torch.float32, (N, H, dk, dv), dev)
+    _check(d_final_state, "d_final_state", torch.float32, (N, H, dk, dv), dev)
+    sizes = (_DTYPES[dt], B, T, Hk, H, dk, dv)
+    with _launching(stream, dev):
+        dqt, dkt, dvt, dgt = (torch.empty_like(x) for x in (q, k, v, g))
+        ds0 = torch.empty((N, H, dk, dv), dtype=torch.float32, device=dev) if d_initial_state else None
+        ws_bytes = lib.kda_linattn_chunk_bwd_workspace_size(*sizes, int(cu_seqlens is not None), N)
+        if ws_bytes == 0:
+            raise KdaError(1, "kda_linattn_chunk_bwd_workspace_size")
+        ws = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
+        rc = lib.kda_linattn_chunk_bwd(*sizes, _ptr(q), _ptr(k), _ptr(v), _ptr(g), per_token, _ptr(cu_seqlens), N,
+                                       _ptr(initial_state), _ptr(d_o), _ptr(d_final_state), _ptr(dqt), _ptr(dkt),
+                                       _ptr(dvt), _ptr(dgt), _ptr(ds0), _ptr(ws), ws_bytes, int(flags),
+                                       _stream(stream, dev))
+    if rc != 0:
+        raise KdaError(rc, "kda_linattn_chunk_bwd")
+    return dqt, dkt, dvt, dgt, ds0
+
+
+class KdaLinAttnFunction(torch.autograd.Function):
+    """Differentiable forward: ``KdaLinAttnFunction.apply(q, k, v, g,
+    cu_seqlens, initial_state)`` returns (o, final_state) from
+    kda_linattn_chunk_fwd; the backward calls kda_linattn_chunk_bwd."""
+
+    @staticmethod
+    def forward(ctx, q, k, v, g, cu_seqlens=None, initial_state=None):
+        o, sf = kda_linattn_chunk_fwd(q, k, v, g, cu_seqlens=cu_seqlens, initial_state=initial_state)
+        ctx.save_for_backward(q, k, v, g, cu_seqlens, initial_state)
+        ctx.set_materialize_grads(False)
+        return o, sf
+
+    @staticmethod
+    def backward(ctx, d_o, d_sf):
+        q, k, v, g, cu_seqlens, initial_state = ctx.saved_tensors
+        d_o = torch.zeros_like(v) if d_o is None else d_o.to(q.dtype).contiguous()
+        dq, dk, dv, dg, ds0 = kda_linattn_chunk_bwd(
+            q, k, v, g, d_o, None if d_sf is None else d_sf.float().contiguous(), cu_seqlens, initial_state,
+            d_initial_state=initial_state is not None and ctx.needs_input_grad[5])
+        return dq, dk, dv, dg, None, ds0
+
+
+def kda_linattn_decode_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor, state: torch.Tensor,
+                            o: Optional[torch.Tensor] = None, flags: int = 0, stream=None):
+    """One step of linear attention with one decay per head for N sequences
+    (C: kda_linattn_decode_step); ``state`` fp32 [N,H,d_k,d_v] is updated in
+    place.  q, k [N,Hk,d_k]; v [N,H,d_v]; g fp32 [N,H] or [H].  Returns o
+    [N,H,d_v]."""
+    dt, dev, Hk, H, dk, dv, per_token = _lin_inputs(q, k, v, g, False)
+    N = q.shape[0]
+    _check(state, "state", torch.float32, (N, H, dk, dv), dev)
+    with _launching(stream, dev):
+        if o is None:
+            o = torch.empty((N, H, dv), dtype=dt, device=dev)
+        _check(o, "o", dt, (N, H, dv), dev)
+        rc = lib.kda_linattn_decode_step(_DTYPES[dt], N, Hk, H, dk, dv, _ptr(q), _ptr(k), _ptr(v), _ptr(g), per_token,
+                                         _ptr(state), _ptr(o), int(flags), _stream(stream, dev))
+    if rc != 0:
+        raise KdaError(rc, "kda_linattn_decode_step")
+    return o
+
+
+def _index(t: Optional[torch.Tensor], name: str, dev):
+    if t is not None and t.dim() != 1:
+        raise ValueError(f"{name} must be a 1-D int32 CUDA tensor")
+    _check(t, name, torch.int32, () if t is None else t.shape, dev)
+
+
+def _cache(codes, scales, dev):
+    if codes.dtype not in CACHE_FORMATS:
+        raise ValueError(f"codes has dtype {codes.dtype}, expected int8 or float8_e4m3fn")
+    if codes.dim() != 4:
+        raise ValueError("codes must be [num_slots,H,d_k,d_v]")
+    _check(codes, "codes", codes.dtype, codes.shape, dev)
+    _check(scales, "scales", torch.float32, codes.shape[:3], dev)
+    return CACHE_FORMATS[codes.dtype]
+
+
+def kda_state_quantize(states: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor,
+                       slots: Optional[torch.Tensor] = None, rows: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Write fp32 states into an 8-bit state cache (C: kda_state_quantize).
+
+    states [M,H,d_k,d_v]; codes [S,H,d_k,d_v] int8 or float8_e4m3fn; scales
+    fp32 [S,H,d_k].  Entry i writes state ``rows[i]`` (i without rows) to slot
+    ``slots[i]`` (i without slots); int32 tensors of one length.  Negative
+    entries are skipped; of several entries for one slot the last is written."""
+    if states.dim() != 4:
+        raise ValueError("states must be [M,H,d_k,d_v]")
+    dev = states.device
+    _check(states, "states", torch.float32, states.shape, dev)
+    fmt = _cache(codes, scales, dev)
+    if codes.shape[1:] != states.shape[1:]:
+        raise ValueError(f"codes has shape {tuple(codes.shape)}, states {tuple(states.shape)}")
+    _index(slots, "slots", dev)
+    _index(rows, "rows", dev)
+    if rows is not None and slots is not None and rows.numel() != slots.numel():
+        raise ValueError(f"{rows.numel()} rows for {slots.numel()} slots")
+    n = slots.numel() if slots is not None else rows.numel() if rows is not None else states.shape[0]
+    M, H, dk, dv = states.shape
+    with _launching(stream, dev):
+        rc = lib.kda_state_quantize(fmt, n, M, codes.shape[0], H, dk, dv, _ptr(states), _ptr(rows), _ptr(slots),
+                                    _ptr(codes), _ptr(scales), _stream(stream, dev))
+    if rc != 0:
+        raise KdaError(rc, "kda_state_quantize")
+
+
+def kda_state_dequantize(codes: torch.Tensor, scales: torch.Tensor, slots: Optional[torch.Tensor] = None,
+                         out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Read states back from an 8-bit state cache (C: kda_state_dequantize):
+    fp32 [n,H,d_k,d_v], state i from slot ``slots[i]`` (every slot in order
+    without slots); zeros for a negative slot."""
+    dev = codes.device
+    fmt = _cache(codes, scales, dev)
+    _index(slots, "slots", dev)
+    S, H, dk, dv = codes.shape
+    n = S if slots is None else slots.numel()
+    with _launching(stream, dev):
+        if out is None:
+            out = torch.empty((n, H, dk, dv), dtype=torch.float32, device=dev)
+        _check(out, "out", torch.float32, (n, H, dk, dv), dev)
+        rc = lib.kda_state_dequantize(fmt, n, S, H, dk, dv, _ptr(codes), _ptr(scales), _ptr(slots), _ptr(out),
+                                      _stream(stream, dev))
+    if rc != 0:
+        raise KdaError(rc, "kda_state_dequantize")
+    return out
 
 
 def kda_check_gates(variant: Union[str, int], gate_range: Union[str, int], alpha: torch.Tensor,

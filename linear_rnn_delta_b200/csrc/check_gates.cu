@@ -53,10 +53,45 @@ __global__ void check_seqlens_kernel(const int32_t *cu, int num_seqs, long long 
     if ((threadIdx.x & 31) == 0 && bad) atomicAdd(count, bad);
 }
 
-// Counters of the synchronous validation (calls hold the mutex below while they use them).
+// Log-decays that are positive or NaN (-infinity, a reset, is allowed).
+__global__ void check_decay_kernel(const float *g, long long n, int *count)
+{
+    int bad = 0;
+    const long long stride = (long long)gridDim.x * blockDim.x;
+    for (long long e = blockIdx.x * (long long)blockDim.x + threadIdx.x; e < n; e += stride)
+        bad += g[e] <= 0.f ? 0 : 1;
+#pragma unroll
+    for (int off = 16; off; off >>= 1) bad += __shfl_xor_sync(0xffffffffu, bad, off);
+    if ((threadIdx.x & 31) == 0 && bad) atomicAdd(count, bad);
+}
+
+// Counters of the synchronous validation (calls hold the mutex while they use them).
 __device__ int g_validate_counts[2];
+std::mutex g_validate_mutex;
 
 }  // namespace
+
+cudaError_t validate_decay(const float *g, long long n, const int32_t *cu, int num_seqs, long long total,
+                           cudaStream_t st, int *bad_gates, int *bad_seqlens)
+{
+    std::lock_guard<std::mutex> lock(g_validate_mutex);
+    int *counts = nullptr;
+    cudaError_t e = cudaGetSymbolAddress(reinterpret_cast<void **>(&counts), g_validate_counts);
+    if (e != cudaSuccess) return e;
+    if ((e = cudaMemsetAsync(counts, 0, 2 * sizeof(int), st)) != cudaSuccess) return e;
+    if (n > 0) {
+        const long long blocks = (n + 255) / 256;
+        check_decay_kernel<<<(unsigned)(blocks < 148 * 16 ? blocks : 148 * 16), 256, 0, st>>>(g, n, counts);
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    }
+    if (cu && (e = launch_check_seqlens(cu, num_seqs, total, counts + 1, st)) != cudaSuccess) return e;
+    int h[2] = {0, 0};
+    if ((e = cudaMemcpyAsync(h, counts, sizeof(h), cudaMemcpyDeviceToHost, st)) != cudaSuccess) return e;
+    if ((e = cudaStreamSynchronize(st)) != cudaSuccess) return e;
+    *bad_gates = h[0];
+    *bad_seqlens = h[1];
+    return cudaSuccess;
+}
 
 cudaError_t launch_check_seqlens(const int32_t *cu, int num_seqs, long long total, int *d_count, cudaStream_t st)
 {
@@ -73,8 +108,7 @@ cudaError_t validate_inputs(int variant, int gate_range, bool bf16, long long n_
                             const void *g1, const int32_t *cu, int num_seqs, long long total, cudaStream_t st,
                             int *bad_gates, int *bad_seqlens)
 {
-    static std::mutex mu;
-    std::lock_guard<std::mutex> lock(mu);
+    std::lock_guard<std::mutex> lock(g_validate_mutex);
     int *counts = nullptr;
     cudaError_t e = cudaGetSymbolAddress(reinterpret_cast<void **>(&counts), g_validate_counts);
     if (e != cudaSuccess) return e;

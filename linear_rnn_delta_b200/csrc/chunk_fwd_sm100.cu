@@ -2840,6 +2840,21 @@ cudaError_t take_device_status(cudaStream_t st, unsigned *bits)
     return cudaSuccess;
 }
 
+cudaError_t device_status_word(unsigned **word)
+{
+    static std::mutex mu;
+    static unsigned *at[64] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    std::lock_guard<std::mutex> lock(mu);
+    if (!at[dev] && (e = cudaGetSymbolAddress(reinterpret_cast<void **>(&at[dev]), g_device_status)) != cudaSuccess)
+        return e;
+    *word = at[dev];
+    return cudaSuccess;
+}
+
 cudaError_t launch_chunk_fwd_sm100(const FwdArgs &a, cudaStream_t st)
 {
     int num_sms = 0;

@@ -90,7 +90,9 @@ cudaError_t launch_check_seqlens(const int32_t *cu, int num_seqs, long long tota
 cudaError_t validate_inputs(int variant, int gate_range, bool bf16, long long n_tok, int dk, const void *alpha,
                             const void *g1, const int32_t *cu, int num_seqs, long long total, cudaStream_t st,
                             int *bad_gates, int *bad_seqlens);
-// Device failure word: read and cleared after `st` has drained.
+// Device failure word: its address on the current device (for kernels of other translation
+// units), and its value, read and cleared after `st` has drained.
+cudaError_t device_status_word(unsigned **word);
 cudaError_t take_device_status(cudaStream_t st, unsigned *bits);
 
 }  // namespace kda

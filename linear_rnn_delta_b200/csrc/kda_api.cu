@@ -5,12 +5,16 @@
 #include <cstdint>
 
 #include "../../include/kda.h"
+#include "api.cuh"
 #include "scan_bwd.cuh"
 #include "rank2.cuh"
 
 namespace {
-
 thread_local char g_detail[512] = "";
+}
+
+namespace kda {
+namespace api {
 
 int fail(int code, const char *fmt, ...)
 {
@@ -26,7 +30,15 @@ int cuda_fail(cudaError_t e, const char *where)
     return fail(KDA_ERR_CUDA, "%s: %s (%s)", where, cudaGetErrorName(e), cudaGetErrorString(e));
 }
 
-bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+}  // namespace api
+}  // namespace kda
+
+namespace {
+
+using kda::api::aligned16;
+using kda::api::cuda_fail;
+using kda::api::fail;
+using kda::api::head_dim_ok;
 
 // Input-preparation flags and their kernel-side bits.
 constexpr unsigned PREP_FLAGS = KDA_FLAG_GATE_LOGITS | KDA_FLAG_L2NORM_K;
@@ -35,7 +47,6 @@ unsigned prep_bits(unsigned flags)
     return ((flags & KDA_FLAG_GATE_LOGITS) ? kda::PREP_LOGITS : 0u) |
            ((flags & KDA_FLAG_L2NORM_K) ? kda::PREP_L2NORM_K : 0u);
 }
-bool head_dim_ok(int d) { return d == 16 || d == 32 || d == 64 || d == 128; }
 bool chunk_ok(int c) { return c == 16 || c == 32 || c == 64 || c == 128; }
 
 // Checks shared by the forward and decode calls: enums, head dims, pointers.
@@ -637,9 +648,10 @@ extern "C" int kda_device_status(void *stream, unsigned *bits)
     const cudaError_t e = kda::take_device_status(static_cast<cudaStream_t>(stream), &w);
     if (e != cudaSuccess) return cuda_fail(e, "kda_device_status");
     if (bits) *bits = w;
-    if (w) return fail(KDA_ERR_DEVICE_TIMEOUT, "device failure bits 0x%x (%s%s)", w,
+    if (w) return fail(KDA_ERR_DEVICE_TIMEOUT, "device failure bits 0x%x (%s%s%s)", w,
                        (w & KDA_DEVICE_WAIT_TIMEOUT) ? "a bounded wait ran out " : "",
-                       (w & KDA_DEVICE_SLOT_MISSING) ? "a chunk slot was not prepared" : "");
+                       (w & KDA_DEVICE_SLOT_MISSING) ? "a chunk slot was not prepared " : "",
+                       (w & KDA_DEVICE_BAD_INDEX) ? "a state-cache index was out of range" : "");
     return KDA_OK;
 }
 

@@ -1,0 +1,97 @@
+// Linear attention with one decay per head: shared definitions of its kernels.
+//
+//   S_t = a_t S_{t-1} + k_t v_t^T,  a_t = e^{g_t},   o_t = S_t^T q_t
+//
+// Every gradient of this recurrence is the same recurrence with its arguments permuted:
+//   dq_t = S_t do_t                                forward in time,  (q, k, v) := (do, v, k), state S^T
+//   dv_t = G_t^T k_t, G_t = a_{t+1} G_{t+1} + q_t do_t^T   backward,  (q, k, v) := (k, q, do), state G
+//   dk_t = G_t v_t                                 backward in time, (q, k, v) := (v, do, q), state G^T
+// with G_t = dL/dS_t (G after the last token = dL/dS_final, dL/dS_initial = a_1 G_1).  One `LinRun`
+// describes one such pass; the kernels know nothing of its role.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace kda {
+
+struct LinRun {
+    // query-, key- and value-like operands [B*T][heads][d], with the value heads per head of theirs
+    const void *x, *y, *z;
+    int gx, gy, gz;             // head of x for value head h: h / gx (x has H / gx heads)
+    const float *g;             // log-decays [B*T][H] (g_ld = H) or [H] (g_ld = 0)
+    int g_ld;
+    const float *s_in;          // [N][H] states or NULL (zero)
+    float *s_out;               // state after the last step (reverse: decayed by the first token too), or NULL
+    int in_t, out_t;            // the stored state is [d_z][d_x] (transposed) instead of [d_x][d_z]
+    float *snap;                // states at boundaries every `snap_tokens` tokens, [slot][H][d_x][d_z], or NULL
+    int snap_tokens;            // (reverse: the state that enters the boundary token, decayed)
+    void *out;                  // [B*T][H][d_z]
+    int out_f32;                // out is fp32 whatever the inputs' type
+    int reverse;                // backward in time
+    int num_seqs, T, H;
+    const int32_t *cu_seqlens;  // packed batch, or NULL (sequence n is rows n*T .. n*T+T-1)
+};
+
+__device__ __forceinline__ int lin_row0(const LinRun &a, int n) { return a.cu_seqlens ? a.cu_seqlens[n] : n * a.T; }
+__device__ __forceinline__ int lin_len(const LinRun &a, int n)
+{
+    return a.cu_seqlens ? a.cu_seqlens[n + 1] - a.cu_seqlens[n] : a.T;
+}
+
+// Tokens between the state boundaries that the gate gradient restarts its sums from.
+constexpr int LIN_SEG = 512;
+
+// Arguments of the backward's closing kernels.
+struct LinGateGrad {
+    const float *dot_q, *dot_k;     // [H][rows]: q.dq and k.dk of every token
+    const float *snap_s, *snap_g;   // boundary states of the dq and dk passes [slot][H][dv][dk]
+    const float *g;                 // log-decays as in LinRun: dg is 0 where the decay is
+    int g_ld;
+    const float *g_end;             // dL/dS_final or NULL: the last boundary of a sequence counts only with it
+    float *dg;                      // [rows][H], or NULL with a decay of each head
+    float *partial;                 // [slot][H] sums over a segment's tokens (decay of each head), or NULL
+    float *dg_head;                 // [H]
+    long long rows;
+    int H, dk, dv, num_seqs, T, slots;
+    const int32_t *cu_seqlens;
+};
+
+cudaError_t launch_lin_scan(const LinRun &r, int dx, int dz, bool bf16, cudaStream_t st);
+// Sums the per-value-head fp32 gradients over the heads that share a key head, casts them, and
+// forms the dots.  dqf, dkf: [rows][H][dk]; dq, dk, q, k: [rows][Hk][dk].
+cudaError_t launch_lin_share(const float *dqf, const float *dkf, const void *q, const void *k, void *dq, void *dk,
+                             float *dot_q, float *dot_k, long long rows, int Hk, int H, int d_k, bool bf16,
+                             cudaStream_t st);
+cudaError_t launch_lin_gate_grad(const LinGateGrad &a, cudaStream_t st);
+
+struct LinDecode {
+    const void *q, *k, *v;
+    const float *g;
+    int g_ld;
+    float *state;
+    void *o;
+    int N, Hk, H, dk, dv;
+};
+cudaError_t launch_lin_decode(const LinDecode &a, bool bf16, cudaStream_t st);
+
+// Counts log-decays that are positive or NaN and violations of the cu_seqlens contract (cu may be
+// NULL), waiting for the verdict on `st` (check_gates.cu).
+cudaError_t validate_decay(const float *g, long long n, const int32_t *cu, int num_seqs, long long total,
+                           cudaStream_t st, int *bad_gates, int *bad_seqlens);
+
+// Quantised state cache.
+struct StateCache {
+    const float *states;    // quantise: [M][H][dk][dv]
+    float *out;             // dequantise: [n][H][dk][dv]
+    uint8_t *codes;         // [S][H][dk][dv]
+    float *scales;          // [S][H][dk]
+    const int32_t *rows, *slots;
+    int n, M, S, H, dk, dv;
+    int format;
+    unsigned *status;       // device failure word
+};
+cudaError_t launch_state_quantize(const StateCache &a, cudaStream_t st);
+cudaError_t launch_state_dequantize(const StateCache &a, cudaStream_t st);
+
+}  // namespace kda
