@@ -31,6 +31,7 @@ struct LinRun {
     int reverse;                // backward in time
     int num_seqs, T, H;
     const int32_t *cu_seqlens;  // packed batch, or NULL (sequence n is rows n*T .. n*T+T-1)
+    long long rows;             // tokens of the whole batch
 };
 
 __device__ __forceinline__ int lin_row0(const LinRun &a, int n) { return a.cu_seqlens ? a.cu_seqlens[n] : n * a.T; }
@@ -58,6 +59,9 @@ struct LinGateGrad {
 };
 
 cudaError_t launch_lin_scan(const LinRun &r, int dx, int dz, bool bf16, cudaStream_t st);
+// Tensor-core form, bf16 only.
+bool lin_chunk_takes(int dx, int dz);
+cudaError_t launch_lin_chunk(const LinRun &r, int dx, int dz, cudaStream_t st);
 // Sums the per-value-head fp32 gradients over the heads that share a key head, casts them, and
 // forms the dots.  dqf, dkf: [rows][H][dk]; dq, dk, q, k: [rows][Hk][dk].
 cudaError_t launch_lin_share(const float *dqf, const float *dkf, const void *q, const void *k, void *dq, void *dk,

@@ -82,7 +82,18 @@ LinRun base_run(const LinSizes &s, const float *g, int g_per_token, const int32_
     r.T = s.T;
     r.H = s.H;
     r.cu_seqlens = cu;
+    r.rows = s.rows;
     return r;
+}
+
+// Tensor-core form for bf16 and the head sizes it takes, else the token scan.
+bool chunk_form(const LinSizes &s, unsigned flags)
+{
+    return s.dtype == KDA_DTYPE_BF16 && !(flags & KDA_FLAG_FORCE_SCAN) && kda::lin_chunk_takes(s.dk, s.dv);
+}
+cudaError_t launch_run(const LinRun &r, int dx, int dz, bool chunk, bool bf16, cudaStream_t st)
+{
+    return chunk ? kda::launch_lin_chunk(r, dx, dz, st) : kda::launch_lin_scan(r, dx, dz, bf16, st);
 }
 
 // Backward workspace regions.
@@ -165,7 +176,7 @@ extern "C" int kda_linattn_chunk_fwd(int dtype, int B, int T, int Hk, int H, int
     r.snap = chunk_states;
     r.snap_tokens = kda::SLOT_TOKENS;
     r.out = o;
-    const cudaError_t e = kda::launch_lin_scan(r, d_k, d_v, dtype == KDA_DTYPE_BF16, st);
+    const cudaError_t e = launch_run(r, d_k, d_v, chunk_form(s, flags), dtype == KDA_DTYPE_BF16, st);
     if (e != cudaSuccess) return cuda_fail(e, "kda_linattn_chunk_fwd launch");
     return KDA_OK;
 }
@@ -209,6 +220,7 @@ extern "C" int kda_linattn_chunk_bwd(int dtype, int B, int T, int Hk, int H, int
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     const bool bf16 = dtype == KDA_DTYPE_BF16;
+    const bool chunk = chunk_form(s, flags);
     const int group = H / Hk;
     auto f32 = [&](size_t off) { return reinterpret_cast<float *>(ws + off); };
     // dq_t = S_t do_t: forward in time, the state transposed
@@ -221,7 +233,7 @@ extern "C" int kda_linattn_chunk_bwd(int dtype, int B, int T, int Hk, int H, int
     r.snap_tokens = kda::LIN_SEG;
     r.out = f32(L.dqf);
     r.out_f32 = 1;
-    cudaError_t e = kda::launch_lin_scan(r, d_v, d_k, bf16, st);
+    cudaError_t e = launch_run(r, d_v, d_k, chunk, bf16, st);
     if (e != cudaSuccess) return cuda_fail(e, "kda_linattn_chunk_bwd dq");
     // dk_t = G_t v_t: backward in time, the state transposed
     r = base_run(s, g, g_per_token, cu_seqlens);
@@ -234,7 +246,7 @@ extern "C" int kda_linattn_chunk_bwd(int dtype, int B, int T, int Hk, int H, int
     r.snap_tokens = kda::LIN_SEG;
     r.out = f32(L.dkf);
     r.out_f32 = 1;
-    if ((e = kda::launch_lin_scan(r, d_v, d_k, bf16, st)) != cudaSuccess) return cuda_fail(e, "kda_linattn_chunk_bwd dk");
+    if ((e = launch_run(r, d_v, d_k, chunk, bf16, st)) != cudaSuccess) return cuda_fail(e, "kda_linattn_chunk_bwd dk");
     // dv_t = G_t^T k_t: backward in time
     r = base_run(s, g, g_per_token, cu_seqlens);
     r.reverse = 1;
@@ -243,7 +255,7 @@ extern "C" int kda_linattn_chunk_bwd(int dtype, int B, int T, int Hk, int H, int
     r.s_in = d_final_state;
     r.s_out = d_initial_state;
     r.out = dv;
-    if ((e = kda::launch_lin_scan(r, d_k, d_v, bf16, st)) != cudaSuccess) return cuda_fail(e, "kda_linattn_chunk_bwd dv");
+    if ((e = launch_run(r, d_k, d_v, chunk, bf16, st)) != cudaSuccess) return cuda_fail(e, "kda_linattn_chunk_bwd dv");
     if ((e = kda::launch_lin_share(f32(L.dqf), f32(L.dkf), q, k, dq, dk, f32(L.dot_q), f32(L.dot_k), s.rows, Hk, H,
                                    d_k, bf16, st)) != cudaSuccess)
         return cuda_fail(e, "kda_linattn_chunk_bwd head sums");
