@@ -73,3 +73,19 @@ def gate_sum_size(q, k, g, mag, dsf_size, cu):
         if dsf_size is not None:
             out[b, lo:hi] += dsf_size[n]
     return out.sum((0, 1)) if g.dim() == 1 else out
+
+
+def pair_size(q, k, z, g, cu=None, back=False):
+    """Sum over the pairs of tokens s <= r of a sequence of |e^{c_r - c_s} (q_r . k_s)| |z|: at r over z_s, or with
+    `back` at s over z_r.  What rounding each pair's weight once can cost o (z = v) or dv (z = d_o)."""
+    B, T, Hk, _ = q.shape
+    H = z.shape[2]
+    out = torch.zeros_like(z)
+    c = g.expand(B, T, H).clamp(min=-1e4)
+    for b, lo, hi in spans(T, B, cu):
+        for h in range(H):
+            cc = c[b, lo:hi, h].cumsum(0)
+            w = torch.exp((cc[:, None] - cc[None, :]).tril()).tril()
+            w = (w * (q[b, lo:hi, h // (H // Hk)] @ k[b, lo:hi, h // (H // Hk)].T)).abs()
+            out[b, lo:hi, h] = (w.T if back else w) @ z[b, lo:hi, h].abs()
+    return out
