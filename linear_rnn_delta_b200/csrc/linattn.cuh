@@ -61,7 +61,8 @@ struct LinGateGrad {
 cudaError_t launch_lin_scan(const LinRun &r, int dx, int dz, bool bf16, cudaStream_t st);
 // Tensor-core form, bf16 only.
 bool lin_chunk_takes(int dx, int dz);
-cudaError_t launch_lin_chunk(const LinRun &r, int dx, int dz, cudaStream_t st);
+cudaError_t launch_lin_chunk(const LinRun &r, int dx, int dz, cudaStream_t st);        // bf16 outputs
+cudaError_t launch_lin_chunk_fine(const LinRun &r, int dx, int dz, cudaStream_t st);   // fp32 outputs
 // Sums the per-value-head fp32 gradients over the heads that share a key head, casts them, and
 // forms the dots.  dqf, dkf: [rows][H][dk]; dq, dk, q, k: [rows][Hk][dk].
 cudaError_t launch_lin_share(const float *dqf, const float *dkf, const void *q, const void *k, void *dq, void *dk,

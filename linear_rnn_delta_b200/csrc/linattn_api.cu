@@ -93,7 +93,7 @@ bool chunk_form(const LinSizes &s, unsigned flags)
 }
 cudaError_t launch_run(const LinRun &r, int dx, int dz, bool chunk, bool bf16, cudaStream_t st)
 {
-    return chunk ? kda::launch_lin_chunk(r, dx, dz, st) : kda::launch_lin_scan(r, dx, dz, bf16, st);
+    return chunk ? (r.out_f32 ? kda::launch_lin_chunk_fine(r, dx, dz, st) : kda::launch_lin_chunk(r, dx, dz, st)) : kda::launch_lin_scan(r, dx, dz, bf16, st);
 }
 
 // Backward workspace regions.

@@ -9,179 +9,85 @@
 // last token, L_rs = e^{c_s - c_r} (s >= r), w_r = e^{c_C - c_r} and u_s = e^{c_s} (which includes the
 // decay of the chunk's first token, so the state handed on enters the token before it).
 //
-// Tensor-core products per chunk, D in tensor memory, lanes = value channel j except for the first:
-//   QK    [r][s]  = X Y^T
-//   KV    [j][i]  = Z^T Ybar          Ybar = u_s y_s in three bf16 parts
-//   inter [j][r]  = R_0^T X^T         R_0^T in two or three bf16 parts, A operand in tensor memory
-//   intra [j][r]  = Z^T P^T           P = L o QK in two bf16 parts
-// x, y, z enter exactly.  What is fp32 and has to be an operand is split into bf16 parts, each the
-// rounding of what the parts before it leave: two parts are off by at most 2^-18 of the value, which is
-// far below the bf16 step of the outputs; the state and what is returned in fp32 take three (2^-27).
-// Decays are differences of running sums kept as two floats each (summed in fp64), so that a strong
-// decay or a reset in a chunk costs the pairs on one side of it nothing.  Log-decays below -10^4 count
-// as -10^4, whose e^g is 0, so that -infinity needs no case of its own.
+// Tensor-core products per chunk; D in tensor memory, lanes = value channel j except for QK:
+//   QK [r][s] = X Y^T
+//   KV [j][i] = (Z^T u) Y           Z^T u, its columns scaled by u_s, in three bf16 parts
+//   O  [j][r] = R_0^T X^T + Z^T P^T   R_0^T in two bf16 parts,  P_rs = (L_rs / w_r) (x_r . y_s) rounded once
+// and out_r = w_r O_r: with the weights divided by w_r the two products share one accumulator.  L_rs / w_r
+// is e^{-c_s}, which stays in range while the chunk's decays multiply to no less than 2^-96 (`narrow`).  A chunk
+// that decays further (a reset, say) has P_rs = L_rs (x_r . y_s), out_r = O_r, and w_r goes to X, rounded.
+// All A operands but QK's are in tensor memory: the tensor core reads 128 bytes of shared memory a cycle,
+// and with A from there, too, operands alone would keep it busy for 1600 cycles a chunk and everybody
+// else's shared-memory accesses waiting.  Z^T gets there from Z by transposing matrix loads.
 //
-// A CTA of 16 warps walks one (sequence, head), one role for each warpgroup and a bounded wait on every
-// mbarrier:
-//   warps 0-1   P: QK lanes 0-63 -> decay, mask, split -> shared memory (row r is a thread's)
-//   warp 2      loads (TMA, three stages of X, Y, Z) and the chunk's decays
-//   warp 3      issues every MMA, in the order KV_i, QK_{i+1}, inter_i, intra_i: the state's way from KV_i
-//               to inter_{i+1} has the other products in between
-//   warps 4-7   Ybar (and Z's rows behind the sequence's end, which belong to the next one: zeroed)
-//   warps 8-11  the state, fp32 in registers (a thread has row j of R^T): R = e^{c_C} R + KV, split
-//   warps 12-15 outputs: w_r inter + intra, rounded and stored (a warp's 32 channels are 64 bytes)
-// Infinities and NaN: masked entries of P are selected, not multiplied, but 0 * NaN in `intra` would
-// carry a token's z to tokens it must not reach.  Warps 4-7 look for them; in a chunk that has any they
-// are taken out of Z and the outputs of that channel from that token on, and the channel's state, become
+// Precision.  x, y, z enter exactly.  A value in n bf16 parts (each the rounding of what the ones before
+// leave) is off by at most 2^-8n of itself: three for what is summed into the fp32 state, two for the state
+// in the outputs, one for P, an error of the outputs' own rounding's size.  Log-decays are summed in fixed
+// point, so that a strong decay costs the pairs on one side of it nothing; those below -10^4 count as
+// -10^4, whose e^g is 0, so that -infinity needs no case of its own.
+//
+// A CTA of 24 warps walks one (sequence, head), with a bounded wait on every mbarrier:
+//   warps 0-1   P: QK lanes 0-63 (a thread has row r) -> decay, mask -> shared memory, two buffers
+//   warp 2      loads (TMA, four stages of X, Y, Z) and the chunk's decays
+//   warp 3      issues every MMA, in the order KV_i, QK_{i+1}, O_i: the state's way from KV_i to O_{i+1} has
+//               the other products in between
+//   warps 4-11  Z^T and its scaled parts to tensor memory
+//   warps 12-15 outputs: w_r O -> bf16 -> [token][channel] tile -> TMA store
+//   warps 16-23 the state, fp32 in registers (a thread has half a row of R^T): R = e^{c_C} R + KV, split
+// Instruction fetch bounds such a kernel as soon as the roles' loops outgrow the SM's instruction cache:
+// loop bodies are kept short (rolled where registers allow), and waits sleep instead of polling.
+// Infinities and NaN: masked entries of P are selected, not multiplied, but 0 * NaN in Z^T P^T would
+// carry a token's z to tokens it must not reach.  Warps 4-11 look for them; in a chunk that has any they
+// are taken out of Z, and the outputs of that channel from that token on, and the channel's state, become
 // NaN instead.
-#include <cuda.h>
-#include <mutex>
-#include <cstring>
-
-#include "common.cuh"
-#include "linattn.cuh"
-#include "sm100.cuh"
+#include "linattn_sm100.cuh"
 
 namespace kda {
 namespace {
 
-using namespace sm100;
+using namespace lin;
 
-constexpr int C = 64;
 constexpr int NT = 768;
-constexpr int NS = 3;                                 // load stages
-constexpr uint32_t TILE = 16384;                      // [64 tokens][128 channels] bf16: two panels of 64 channels
-constexpr uint32_t STAGE = 3 * TILE;                  // X, Y, Z
-constexpr uint32_t SM_KB = NS * STAGE;                // Ybar, three parts
-constexpr uint32_t SM_P = SM_KB + 3 * TILE;           // P: two tiles of [64][64] bf16 (two chunks', or two parts)
+constexpr int NS = 4;                                 // load stages
+constexpr uint32_t SM_P = NS * STAGE;                 // P, two chunks' [64][64] bf16
 constexpr uint32_t SM_GATE = SM_P + 2 * 8192;
 struct GateStage {
     float2 c[C];        // running sums of log2-decays, two floats
-    float a[C], b[C];   // 2^{c_r - m}, 2^{m - c_s} with m half the chunk's sum: their product is L_rs (`narrow`)
-    float w_in[C];      // w_r
-    float w_out[C];     // u_s
+    float b[C];         // L_rs / w_r
+    float w[C];         // w_r
+    float u[C];         // u_s
     float total;        // e^{c_C}
     int nv;             // tokens of the chunk
     int bad;            // Z holds an infinity or a NaN
-    int narrow;         // a and b are within 2^100 of 1
+    int narrow;
     short from[128];    // ... of channel j, first (backward: last) token
 };
 constexpr uint32_t SM_BAR = SM_GATE + NS * sizeof(GateStage);
-enum { B_FULL = 0, B_GATE = NS, B_EMPTY = 2 * NS, B_QKF = 3 * NS, B_QKE = B_QKF + 2, B_PF = B_QKE + 2, B_OF = B_PF + 2,
-       B_KBF = B_OF + 2, B_KVF, B_KVE, B_SF, B_SE, B_OE, B_DRAIN, NBAR };
+enum { B_FULL = 0, B_GATE = NS, B_EMPTY = 2 * NS, B_QKF = 3 * NS, B_QKE, B_PF, B_OF = B_PF + 2, B_KBF = B_OF + 2, B_ZF,
+       B_KVF, B_KVE, B_SF, B_SE, B_OE, B_DRAIN, NBAR };
 constexpr uint32_t SM_MISC = SM_BAR + NBAR * 8;       // tensor-memory address, abort flag
 constexpr uint32_t SM_ALLOC = SM_MISC + 16 + 1024;
 static_assert(SM_ALLOC <= 232448, "shared memory budget");
 
+constexpr long long NARROW = 96ll << 32;   // leaves x . y 31 binary orders before e^{-c_s} (x . y) overflows
+
 // registers of the six warpgroups: what they give up or take adds up to the launch's 80 each
-constexpr int RG_P = 72, RG_YBAR = 64, RG_OUT = 72, RG_STATE = 104;
-static_assert(RG_P + 2 * RG_YBAR + RG_OUT + 2 * RG_STATE <= 6 * 80, "more registers than the block has");
+constexpr int RG_P = 72, RG_Z = 72, RG_OUT = 56, RG_STATE = 104;
+static_assert(RG_P + 2 * RG_Z + RG_OUT + 2 * RG_STATE <= 6 * 80, "more registers than the block has");
 
-// tensor-memory columns: KV, the state's parts, inter, intra, QK.  With two parts QK has room for two chunks
-constexpr uint32_t TM_KV = 0, TM_S = 128, TM_COLS = 512;
-__host__ __device__ constexpr uint32_t tm_inter(int nsp) { return TM_S + 64 * nsp; }
-__host__ __device__ constexpr uint32_t tm_intra(int nsp) { return tm_inter(nsp) + 64; }
-__host__ __device__ constexpr uint32_t tm_qk(int nsp) { return tm_intra(nsp) + 64; }
-
-constexpr long long WAIT_LIMIT = 1ll << 32;           // cycles, about 2 s
-constexpr unsigned DEV_WAIT_TIMEOUT = 1u;
-constexpr double LOG2E = 1.4426950408889634;
+// tensor-memory columns: KV, O, QK, the state's two parts, the scaled Z^T's three, Z^T
+constexpr uint32_t TM_KV = 0, TM_O = 128, TM_QK = 192, TM_S = 256, TM_ZP = 384, TM_Z = 480, TM_COLS = 512;
 
 struct LinChunkParams {
     LinRun a;
-    CUtensorMap tx, ty, tz;
+    CUtensorMap tx, ty, tz, to;
     unsigned *status;
 };
 
-// K-major descriptor, K step kk of 16 elements, panels of 64 elements `pstride` bytes apart
-__device__ __forceinline__ uint64_t dK(uint32_t base, int kk)
-{
-    return make_desc_sw128(base, 16) + (uint64_t)(((uint32_t)(kk >> 2) * 8192u + (uint32_t)(kk & 3) * 32u) >> 4);
-}
-// MN-major descriptor of a [token][channel] tile (two panels of 64 channels), K step kk of 16 tokens
-__device__ __forceinline__ uint64_t dMN(uint32_t base, int kk)
-{
-    return make_desc_sw128(base, 8192) + (uint64_t)((uint32_t)kk * (2048u >> 4));
-}
-
-// Waits for a phase; false if the wait ran out here (recorded for the others) or elsewhere.
-__device__ __forceinline__ bool wait_one(uint64_t *bar, uint32_t parity, volatile int *abort)   // one thread
-{
-    const long long t0 = clock64();
-    while (!mbar_try_wait(bar, parity)) {
-        if (*abort) return false;
-        if (clock64() - t0 > WAIT_LIMIT) {
-            *abort = 1;
-            return false;
-        }
-    }
-    return true;
-}
-__device__ __forceinline__ bool wait_slow(uint64_t *bar, uint32_t parity, volatile int *abort)
-{
-    const long long t0 = clock64();
-    for (;;) {
-        if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity) != 0)) return true;
-        if (__any_sync(0xffffffffu, *abort != 0 || clock64() - t0 > WAIT_LIMIT)) {
-            *abort = 1;
-            return false;
-        }
-    }
-}
-__device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, volatile int *abort)   // a warp, one answer
-{
-    return __all_sync(0xffffffffu, mbar_try_wait(bar, parity) != 0) || wait_slow(bar, parity, abort);
-}
-__device__ __forceinline__ void warp_arrive(uint64_t *bar)   // one arrival for the warp, behind all its lanes
-{
-    __syncwarp();
-    if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
-}
-
-__device__ __forceinline__ float2 unpack(uint32_t w)
-{
-    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
-}
-// next bf16 part of a pair: rounds x, leaves the rest in x
-__device__ __forceinline__ uint32_t take_part(float2 &x)
-{
-    const uint32_t w = pack_bf16(x.x, x.y);
-    x = __ffma2_rn(unpack(w), make_float2(-1.f, -1.f), x);
-    return w;
-}
-__device__ __forceinline__ float ex2(float x)
-{
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-// 2^x, the error that of exp2f on [-1/2, 1/2] whatever the size of x
-__device__ __forceinline__ float exp2_wide(double x)
-{
-    if (!(x > -126.0 && x < 127.0)) return exp2f((float)x);   // (nearly) nothing, overflow or NaN
-    const double n = rint(x);
-    return exp2f((float)(x - n)) * __int_as_float(((int)n + 127) << 23);
-}
-__device__ __forceinline__ float diff(float2 a, float2 b) { return (a.x - b.x) + (a.y - b.y); }
-
-// max of the magnitudes of two bf16 pairs, NaN if either is one
-__device__ __forceinline__ uint32_t max_abs2(uint32_t x, uint32_t y)
-{
-    uint32_t r;
-    asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
-    return r;
-}
-
-// NSP: bf16 parts of the state in `inter`.  NPP: parts of P; with one, P and its accumulator have two
-// buffers each and the next chunk's P is formed while this one's is multiplied.
-template <int DX, int DZ, int NSP, int NPP, typename TOut>
+template <int DX, int DZ>
 __global__ void __launch_bounds__(NT, 1) lin_chunk_kernel(const __grid_constant__ LinChunkParams P)
 {
     constexpr int JW = DZ / 32;                // warps with value channels of their own
-    constexpr int NB = NPP == 1 ? 2 : 1;       // buffers of P and QK
-    constexpr bool BF16_OUT = sizeof(TOut) == 2;
-    constexpr uint32_t TM_INTER = tm_inter(NSP), TM_INTRA = tm_intra(NSP), TM_QK = tm_qk(NSP);
-    static_assert(TM_QK + 64 * NB <= TM_COLS, "tensor memory");
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     const uint32_t sb = smem_u32(sm);
@@ -203,15 +109,16 @@ __global__ void __launch_bounds__(NT, 1) lin_chunk_kernel(const __grid_constant_
         for (int s = 0; s < NS; ++s) {
             mbar_init(bar + B_FULL + s, 1);
             mbar_init(bar + B_GATE + s, 1);
-            mbar_init(bar + B_EMPTY + s, 1 + 2 * JW + (BF16_OUT ? 4 : JW));
+            mbar_init(bar + B_EMPTY + s, 1 + 2 * JW + 4);   // products, state, outputs
         }
+        mbar_init(bar + B_QKF, 1);
+        mbar_init(bar + B_QKE, 2);
         for (int s = 0; s < 2; ++s) {
-            mbar_init(bar + B_QKF + s, 1);
-            mbar_init(bar + B_QKE + s, 2);
             mbar_init(bar + B_PF + s, 2);
             mbar_init(bar + B_OF + s, 1);
         }
         mbar_init(bar + B_KBF, 8);
+        mbar_init(bar + B_ZF, 8);
         mbar_init(bar + B_KVF, 1);
         mbar_init(bar + B_KVE, 2 * JW);
         mbar_init(bar + B_SF, 2 * JW);
@@ -227,8 +134,6 @@ __global__ void __launch_bounds__(NT, 1) lin_chunk_kernel(const __grid_constant_
     const uint32_t tlane = tbase + ((uint32_t)((warp & 3) * 32) << 16);
     // chunk of iteration i
     auto chunk = [&](int i) { return rev ? nch - 1 - i : i; };
-    // phase parity of the i-th use of a barrier that alternates between NB
-    auto par = [](int i) { return (uint32_t)(i / NB) & 1u; };
 
     if (wg == 0) {
         regs_dec<RG_P>();
@@ -236,78 +141,61 @@ __global__ void __launch_bounds__(NT, 1) lin_chunk_kernel(const __grid_constant_
             // ---- P: row r of QK
             const int r = tid;
             for (int i = 0; i < nch; ++i) {
-                const int s = i % NS, pb = i % NB;
+                const int s = i % NS, pb = i & 1;
                 const GateStage &G = gates[s];
-                // P's buffer is free once intra_{i-NB} has read it
-                if (!wait(bar + B_GATE + s, (i / NS) & 1, s_abort) || !wait(bar + B_QKF + pb, par(i), s_abort) ||
-                    (i >= NB && !wait(bar + B_OF + pb, par(i - NB), s_abort)))
+                // P's buffer is free once O_{i-2} has read it
+                if (!wait(bar + B_GATE + s, (i / NS) & 1, s_abort) || !wait(bar + B_QKF, i & 1, s_abort) ||
+                    (i >= 2 && !wait(bar + B_OF + pb, ((i >> 1) - 1) & 1, s_abort)))
                     break;
                 tc_fence_after();
                 const int first = rev ? r : 0, last = rev ? G.nv - 1 : r;   // the row's tokens
-                // columns that no row of the warp masks
-                const int clear_from = rev ? warp * 32 + 31 : 0, clear_to = rev ? G.nv - 1 : warp * 32;
                 const float2 cr = G.c[r];
                 const bool narrow = G.narrow != 0;
-                const float af = rev ? G.b[r] : G.a[r];
-                const float2 ar = make_float2(af, af);
-                const float *bcol = rev ? G.a : G.b;
                 uint8_t *prow = sm + SM_P + pb * 8192 + r * 128;
 #pragma unroll 1
-                for (int blk = 0; blk < 4; ++blk) {
-                    uint32_t hi[8], lo[NPP == 2 ? 8 : 1];
-                    if (rev ? blk * 16 + 15 < warp * 32 : blk * 16 > warp * 32 + 31) {   // masked for all of the warp's rows
+                for (int half = 0; half < 2; ++half) {
+                    uint32_t pk[16];
+                    if (rev ? half < warp : half > warp) {   // masked for all of the warp's rows
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            hi[e] = 0u;
-                            if (NPP == 2) lo[e] = 0u;
-                        }
+                        for (int e = 0; e < 16; ++e) pk[e] = 0u;
                     } else {
-                        float2 v[8];
-                        tmem_ld16(tlane + TM_QK + pb * 64 + blk * 16, &v[0].x);
+                        float2 v[16];
+                        tmem_ld32(tlane + TM_QK + half * 32, &v[0].x);
                         tmem_wait_ld();
                         if (narrow) {
 #pragma unroll
-                            for (int e = 0; e < 8; e += 2) {
-                                const float4 bs = *reinterpret_cast<const float4 *>(bcol + blk * 16 + 2 * e);
-                                v[e] = __fmul2_rn(__fmul2_rn(v[e], ar), make_float2(bs.x, bs.y));
-                                v[e + 1] = __fmul2_rn(__fmul2_rn(v[e + 1], ar), make_float2(bs.z, bs.w));
+                            for (int e = 0; e < 16; e += 2) {
+                                const float4 bs = *reinterpret_cast<const float4 *>(&G.b[half * 32 + 2 * e]);
+                                v[e] = __fmul2_rn(v[e], make_float2(bs.x, bs.y));
+                                v[e + 1] = __fmul2_rn(v[e + 1], make_float2(bs.z, bs.w));
                             }
                         } else {   // a strong decay or a reset in the chunk: each pair's own exponential
 #pragma unroll
-                            for (int e = 0; e < 8; ++e) {
-                                const float4 cs = *reinterpret_cast<const float4 *>(&G.c[blk * 16 + 2 * e]);
+                            for (int e = 0; e < 16; ++e) {
+                                const float4 cs = *reinterpret_cast<const float4 *>(&G.c[half * 32 + 2 * e]);
                                 const float d0 = diff(cr, make_float2(cs.x, cs.y)), d1 = diff(cr, make_float2(cs.z, cs.w));
                                 v[e].x *= ex2(rev ? -d0 : d0);
                                 v[e].y *= ex2(rev ? -d1 : d1);
                             }
                         }
-                        if (blk * 16 + 15 > clear_to || blk * 16 < clear_from) {
+                        if (half == warp || (rev && G.nv < C)) {   // columns that some row of the warp masks
 #pragma unroll
-                            for (int e = 0; e < 8; ++e) {
-                                const int s0 = blk * 16 + 2 * e;
+                            for (int e = 0; e < 16; ++e) {
+                                const int s0 = half * 32 + 2 * e;
                                 if (s0 < first || s0 > last) v[e].x = 0.f;
                                 if (s0 + 1 < first || s0 + 1 > last) v[e].y = 0.f;
                             }
                         }
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            if (NPP == 2) {
-                                hi[e] = take_part(v[e]);
-                                lo[e] = pack_bf16(v[e].x, v[e].y);
-                            } else {
-                                hi[e] = pack_bf16(v[e].x, v[e].y);
-                            }
-                        }
+                        for (int e = 0; e < 16; ++e) pk[e] = pack_bf16(v[e].x, v[e].y);
                     }
 #pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        uint4 *at = reinterpret_cast<uint4 *>(prow + (((blk * 2 + q) ^ (r & 7)) << 4));
-                        at[0] = make_uint4(hi[4 * q], hi[4 * q + 1], hi[4 * q + 2], hi[4 * q + 3]);
-                        if (NPP == 2) at[512] = make_uint4(lo[4 * q], lo[4 * q + 1], lo[4 * q + 2], lo[4 * q + 3]);
-                    }
+                    for (int q = 0; q < 4; ++q)
+                        *reinterpret_cast<uint4 *>(prow + (((half * 4 + q) ^ (r & 7)) << 4)) =
+                            make_uint4(pk[4 * q], pk[4 * q + 1], pk[4 * q + 2], pk[4 * q + 3]);
                 }
                 tc_fence_before();
-                warp_arrive(bar + B_QKE + pb);
+                warp_arrive(bar + B_QKE);
                 fence_async_smem();
                 warp_arrive(bar + B_PF + pb);
             }
@@ -340,36 +228,44 @@ __global__ void __launch_bounds__(NT, 1) lin_chunk_kernel(const __grid_constant_
                         tma_load_3d(st + 2 * TILE + p * 8192, &P.tz, bar + B_FULL + s, p * 64, h / a.gz, row0 + t0);
                 }
                 GateStage &G = gates[s];
-                const int nv = min(C, len - t0);
-                double g2[2];
-#pragma unroll
-                for (int e = 0; e < 2; ++e) g2[e] = (double)(next[e] < -1e4f ? -1e4f : next[e]) * LOG2E;   // NaN stays
+                // e^g is 0 far before -10^4 (and infinite before 10^4, which breaks the contract)
+                const float ga = fminf(fmaxf(next[0], -1e4f), 1e4f), gb = fminf(fmaxf(next[1], -1e4f), 1e4f);
+                const unsigned nan_a = __ballot_sync(0xffffffffu, next[0] != next[0]);
+                const unsigned nan_b = __ballot_sync(0xffffffffu, next[1] != next[1]);
                 if (i + 1 < nch) gate_load(i + 1);
-                double run = g2[0] + g2[1];
-#pragma unroll
+                const long long fb = fix_log2(gb);
+                long long run = fix_log2(ga) + fb;
+#pragma unroll 1
                 for (int off = 1; off < 32; off <<= 1) {
-                    const double o = __shfl_up_sync(0xffffffffu, run, off);
+                    const long long o = __shfl_up_sync(0xffffffffu, run, off);
                     if (lane >= off) run += o;
                 }
-                const double end = __shfl_sync(0xffffffffu, run, 31), mid = 0.5 * end;
-                bool narrow = true;
-#pragma unroll
+                const long long end = __shfl_sync(0xffffffffu, run, 31);
+                const float nan = __int_as_float(0x7fc00000);
+                bool narrow = (nan_a | nan_b) == 0;
+#pragma unroll 1
                 for (int e = 0; e < 2; ++e) {
                     const int t = 2 * lane + e;
-                    const double c = e ? run : run - g2[1];
-                    const float hi = (float)c;
-                    G.c[t] = make_float2(hi, (float)(c - (double)hi));
-                    G.a[t] = exp2_wide(c - mid);
-                    G.b[t] = exp2_wide(mid - c);
-                    narrow = narrow && c - mid < 100.0 && mid - c < 100.0;
-                    const float since = exp2_wide(c), left = exp2_wide(end - c);
-                    G.w_in[t] = rev ? left : since;
-                    G.w_out[t] = rev ? since : left;
+                    const long long c = e ? run : run - fb, left = end - c;
+                    float2 cc = make_float2((float)fix_int(c), fix_rest(c));
+                    float w = fix_exp2(rev ? left : c), u = fix_exp2(rev ? c : left);
+                    narrow = narrow && c < NARROW && -c < NARROW && left < NARROW && -left < NARROW;
+                    G.b[t] = fix_exp2(rev ? -left : -c);
+                    if (nan_a | nan_b) {   // a NaN decay is part of every sum from its token on
+                        const unsigned upto = 0xffffffffu >> (31 - lane);
+                        const bool seen = (nan_a & upto) || (nan_b & (e ? upto : upto >> 1));
+                        if (seen) cc.x = nan;
+                        if (seen || rev) w = nan;
+                        if (seen || !rev) u = nan;
+                    }
+                    G.c[t] = cc;
+                    G.w[t] = w;
+                    G.u[t] = u;
                 }
                 narrow = __all_sync(0xffffffffu, narrow);
                 if (lane == 0) {
-                    G.total = exp2_wide(end);
-                    G.nv = nv;
+                    G.total = (nan_a | nan_b) ? nan : fix_exp2(end);
+                    G.nv = min(C, len - t0);
                     G.narrow = narrow;
                 }
                 warp_arrive(bar + B_GATE + s);
@@ -377,241 +273,265 @@ __global__ void __launch_bounds__(NT, 1) lin_chunk_kernel(const __grid_constant_
             // no load is in flight when the CTA ends, wound down early or not
             if (lane == 0)
                 for (int j = max(0, i - NS); j < i; ++j) mbar_wait_cycles(bar + B_FULL + j % NS, (j / NS) & 1, WAIT_LIMIT);
-        } else if (lane == 0) {
+        } else {
             // ---- MMA issue
-            constexpr uint32_t ID_QK = idesc_bf16(128, C, false, false), ID_KV = idesc_bf16(128, DX, true, true);
-            constexpr uint32_t ID_INTER = idesc_bf16(128, C, false, false), ID_INTRA = idesc_bf16(128, C, true, false);
+            const uint32_t lead = lane == 0;
+            constexpr uint32_t ID_QK = idesc_bf16(128, C, false, false), ID_KV = idesc_bf16(128, DX, false, true);
+            constexpr uint32_t ID_O = idesc_bf16(128, C, false, false);
+            const uint32_t pt = k_tile(sb + SM_P);
             bool ok = true;
-            auto qk = [&](int i) {   // rows 64-127 of A are what lies behind X: lanes nobody reads
-                const uint32_t st = sb + (i % NS) * STAGE, d = tbase + TM_QK + (i % NB) * 64;
-                ok = ok && wait_one(bar + B_FULL + i % NS, (i / NS) & 1, s_abort);
-                if (i >= NB) ok = ok && wait_one(bar + B_QKE + i % NB, par(i - NB), s_abort);
-                if (!ok) return;
-                tc_fence_after();
-#pragma unroll
-                for (int kk = 0; kk < DX / 16; ++kk) mma_bf16(d, dK(st, kk), dK(st + TILE, kk), ID_QK, kk > 0);
-                mma_commit(bar + B_QKF + i % NB);
-            };
             for (int i = -1; i < nch && ok; ++i) {
                 const uint32_t st = sb + ((i + NS) % NS) * STAGE;
                 if (i >= 0) {
-                    ok = wait_one(bar + B_KBF, i & 1, s_abort) &&
-                         (i == 0 || wait_one(bar + B_KVE, (i - 1) & 1, s_abort));
+                    ok = wait(bar + B_KBF, i & 1, s_abort) && (i == 0 || wait(bar + B_KVE, (i - 1) & 1, s_abort));
                     if (!ok) break;
                     tc_fence_after();
+                    const uint32_t y = mn_tile(st + TILE);
 #pragma unroll 1
                     for (int p = 0; p < 3; ++p)
 #pragma unroll
                         for (int kk = 0; kk < C / 16; ++kk)
-                            mma_bf16(tbase + TM_KV, dMN(st + 2 * TILE, kk), dMN(sb + SM_KB + p * TILE, kk), ID_KV, p + kk > 0);
-                    mma_commit(bar + B_KVF);
+                            mma_bf16_ts_warp(tbase + TM_KV, tbase + TM_ZP + p * 32 + kk * 8, dMN(y, kk), ID_KV, p + kk > 0, lead);
+                    mma_commit_warp(bar + B_KVF, lead);
                 }
-                if (i + 1 < nch) qk(i + 1);
+                if (i + 1 < nch) {   // QK of the next one; rows 64-127 of A are what lies behind X: lanes nobody reads
+                    const int sn = (i + 1) % NS;
+                    const uint32_t x = k_tile(sb + sn * STAGE), y = k_tile(sb + sn * STAGE + TILE);
+                    ok = wait(bar + B_FULL + sn, ((i + 1) / NS) & 1, s_abort) &&
+                         (i < 0 || wait(bar + B_QKE, i & 1, s_abort));
+                    if (!ok) break;
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int p = 0; p < DX / 64; ++p)
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+                            mma_bf16_warp(tbase + TM_QK, dK(x, kk) + p * 512, dK(y, kk) + p * 512, ID_QK, p + kk > 0, lead);
+                    mma_commit_warp(bar + B_QKF, lead);
+                }
                 if (i < 0) continue;
-                ok = ok && wait_one(bar + B_SF, i & 1, s_abort) &&
-                     (i == 0 || wait_one(bar + B_OE, (i - 1) & 1, s_abort));
+                ok = wait(bar + B_SF, i & 1, s_abort) && (i == 0 || wait(bar + B_OE, (i - 1) & 1, s_abort));
                 if (!ok) break;
                 tc_fence_after();
+                const uint32_t x = k_tile(st);
 #pragma unroll 1
-                for (int p = 0; p < NSP; ++p)
+                for (int p = 0; p < 2 * (DX / 64); ++p) {   // a part's panel of 64 key channels
+                    const int part = p / (DX / 64), panel = p % (DX / 64);
 #pragma unroll
-                    for (int kk = 0; kk < DX / 16; ++kk)
-                        mma_bf16_ts(tbase + TM_INTER, tbase + TM_S + p * 64 + kk * 8, dK(st, kk), ID_INTER, p + kk > 0);
-                mma_commit(bar + B_SE);
-                ok = wait_one(bar + B_PF + i % NB, par(i), s_abort);
+                    for (int kk = 0; kk < 4; ++kk)
+                        mma_bf16_ts_warp(tbase + TM_O, tbase + TM_S + part * 64 + panel * 32 + kk * 8, dK(x, kk) + panel * 512,
+                                         ID_O, p + kk > 0, lead);
+                }
+                mma_commit_warp(bar + B_SE, lead);
+                ok = wait(bar + B_PF + (i & 1), (i >> 1) & 1, s_abort) && wait(bar + B_ZF, i & 1, s_abort);
                 if (!ok) break;
                 tc_fence_after();
-#pragma unroll 1
-                for (int p = 0; p < NPP; ++p)
 #pragma unroll
-                    for (int kk = 0; kk < C / 16; ++kk)
-                        mma_bf16(tbase + TM_INTRA, dMN(st + 2 * TILE, kk), dK(sb + SM_P + (i % NB + p) * 8192, kk), ID_INTRA,
-                                 p + kk > 0);
-                mma_commit(bar + B_OF + i % NB);
-                mma_commit(bar + B_EMPTY + i % NS);
+                for (int kk = 0; kk < C / 16; ++kk)
+                    mma_bf16_ts_warp(tbase + TM_O, tbase + TM_Z + kk * 8, dK(pt + (i & 1) * 512, kk), ID_O, 1, lead);
+                mma_commit_warp(bar + B_OF + (i & 1), lead);
+                mma_commit_warp(bar + B_EMPTY + i % NS, lead);
             }
             // products still running are waited for below (every product of a full run is, by its readers)
             if (!ok) {
-                mma_commit(bar + B_DRAIN);
-                mbar_wait_cycles(bar + B_DRAIN, 0, WAIT_LIMIT);
+                mma_commit_warp(bar + B_DRAIN, lead);
+                if (lane == 0) mbar_wait_cycles(bar + B_DRAIN, 0, WAIT_LIMIT);
             }
         }
     } else if (wg <= 2) {
-        regs_dec<RG_YBAR>();
-        // ---- Ybar
-        constexpr int YT = 256;
-        const int t = tid - 128;
+        regs_dec<RG_Z>();
+        // ---- Z^T and its scaled parts: a warp has 32 channels and (by warpgroup) half of the tokens
+        constexpr int ZT = 256;
+        const int t = tid - 128, q = warp & 3, part0 = (wg - 1) * 16;   // columns of 2 tokens
+        // this lane's row of the first 8x8 piece (a piece of 16 more tokens is 2048 bytes on, of 16 more
+        // channels two 16-byte columns on, under the swizzle)
+        const int ch = (q & 1) * 4 + ((lane >> 3) & 1), zr = (lane >> 4) * 8 + (lane & 7);
+        const uint32_t zaddr = sb + 2 * TILE + (q >> 1) * 8192 + (wg - 1) * 4096 + zr * 128 + ((ch ^ (zr & 7)) << 4);
+        const uint32_t zstep = (((ch + 2) ^ (zr & 7)) << 4) - ((ch ^ (zr & 7)) << 4);
         bool ok = true;
         for (int i = 0; i < nch; ++i) {
             const int s = i % NS;
             GateStage &G = gates[s];
             uint8_t *st = sm + s * STAGE;
             ok = ok && wait(bar + B_GATE + s, (i / NS) & 1, s_abort) && wait(bar + B_FULL + s, (i / NS) & 1, s_abort);
-            if (!group_sync_and(1, YT, ok)) break;   // the group's barriers need all of it
+            if (!group_sync_and(1, ZT, ok)) break;   // the group's barriers need all of it: it gives up together
             const int nv = G.nv;
-            // rows behind the sequence's end belong to another one (or hold nothing): zero
+            // rows of Y and Z behind the sequence's end belong to another one (or hold nothing): zero
             if (nv < C) {
-                for (int e = t; e < (DZ / 64) * (C - nv) * 8; e += YT) {
-                    const int p = e / ((C - nv) * 8), q = e % ((C - nv) * 8);
-                    *reinterpret_cast<uint4 *>(st + 2 * TILE + p * 8192 + nv * 128 + q * 16) = make_uint4(0, 0, 0, 0);
-                }
-                group_sync(1, YT);
-            }
-            uint32_t most = 0;
-#pragma unroll
-            for (int q = 0; q < DZ / 32; ++q) {
-                const uint4 w = *reinterpret_cast<const uint4 *>(st + 2 * TILE + (t + YT * q) * 16);
-                most = max_abs2(max_abs2(most, max_abs2(w.x, w.y)), max_abs2(w.z, w.w));
-            }
-            const bool clean = group_sync_and(1, YT, (most & 0x7fffu) < 0x7f80u && (most & 0x7fff0000u) < 0x7f800000u);
-            if (t == 0) G.bad = !clean;
-            if (!clean && t < 128) {
-                int from = rev ? -1 : C;
-                if (t < DZ) {
-                    for (int u = 0; u < C; ++u) {
-                        const int r = rev ? u : C - 1 - u;   // the last write is the first token in time
-                        uint8_t *at = st + 2 * TILE + (t >> 6) * 8192 + r * 128 + (((t & 63) * 2) ^ ((r & 7) << 4));
-                        unsigned short &w = *reinterpret_cast<unsigned short *>(at);
-                        if ((w & 0x7f80u) == 0x7f80u) {
-                            w = 0;
-                            from = r;
-                        }
-                    }
-                }
-                G.from[t] = (short)from;
-            }
-            ok = i == 0 || wait(bar + B_KVF, (i - 1) & 1, s_abort);   // KV_{i-1} has read Ybar
-            if (!ok) continue;
-#pragma unroll 2
-            for (int q = 0; q < DX / 32; ++q) {
-                const int off = (t + YT * q) * 16, r = (off & 8191) >> 7;
-                uint4 w = *reinterpret_cast<const uint4 *>(st + TILE + off);
-                if (r >= nv) w = make_uint4(0, 0, 0, 0);
-                const float u = G.w_out[r];
-                const float2 u2 = make_float2(u, u);
-                uint32_t part[3][4];
-                const uint32_t in[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    float2 x = __fmul2_rn(unpack(in[e]), u2);
-                    part[0][e] = take_part(x);
-                    part[1][e] = take_part(x);
-                    part[2][e] = pack_bf16(x.x, x.y);
-                }
-#pragma unroll
-                for (int p = 0; p < 3; ++p)
-                    *reinterpret_cast<uint4 *>(sm + SM_KB + p * TILE + off) =
-                        make_uint4(part[p][0], part[p][1], part[p][2], part[p][3]);
-            }
-            fence_async_smem();
-            warp_arrive(bar + B_KBF);
-        }
-    } else if (wg == 3) {
-        regs_dec<RG_OUT>();
-        // ---- outputs
-        const size_t ld = (size_t)a.H * DZ;
-        if constexpr (BF16_OUT) {
-            // Fragments of O^T (channel, token pair) go transposed into [token][channel] rows over this
-            // stage's X and Y, which nobody reads any more; rows of DZ channels then leave by bulk copies.
-            constexpr uint32_t RS = DZ * 2 + 16;   // the 16 bytes spread 8 rows over all banks
-            const int q = warp & 3;
-            bool ok = true;
-            for (int i = 0; i < nch; ++i) {
-                const int s = i % NS, t0 = chunk(i) * C;
-                ok = wait(bar + B_OF + i % NB, par(i), s_abort);
-                if (!group_sync_and(2, 128, ok)) break;
-                tc_fence_after();
-                const GateStage &G = gates[s];
-                const int nv = G.nv;
-                const uint32_t stage = sb + s * STAGE;
-                if (q < JW) {
-                    const bool bad = G.bad != 0;
+                const int rest = (C - nv) * 8;
 #pragma unroll 1
-                    for (int x = 0; x < 4; ++x) {
-                        const int half = x >> 1, g = x & 1;   // 32 tokens, 16 channels
-                        float u[16], v[16];
-                        const uint32_t at = tlane + ((uint32_t)(g * 16) << 16) + half * 32;
-                        tmem_ld_frag4(at + TM_INTER, u);
-                        tmem_ld_frag4(at + TM_INTRA, v);
-                        tmem_wait_ld();
-                        if (x == 3) {   // the accumulators are read
-                            tc_fence_before();
-                            warp_arrive(bar + B_OE);
-                        }
-                        uint32_t pk[8];
+                for (int e = t; e < (DX / 64 + DZ / 64) * rest; e += ZT) {
+                    const int p = e / rest;
+                    *reinterpret_cast<uint4 *>(st + TILE + (p < DX / 64 ? p : p - DX / 64 + 2) * 8192 + nv * 128 +
+                                               e % rest * 16) = make_uint4(0, 0, 0, 0);
+                }
+                fence_async_smem();
+                group_sync(1, ZT);
+            }
+            uint32_t z[2][8];   // 16 channels, 32 tokens each
+            bool clean = true;
+#pragma unroll 1
+            for (int pass = 0;; ++pass) {
+                uint32_t most = 0;
+                if (q < JW) {
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const float2 w = *reinterpret_cast<const float2 *>(&G.w_in[half * 32 + k * 8 + 2 * (lane & 3)]);
+                    for (int g = 0; g < 2; ++g)
 #pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                float2 o = __ffma2_rn(make_float2(u[4 * k + 2 * e], u[4 * k + 2 * e + 1]), w,
-                                                      make_float2(v[4 * k + 2 * e], v[4 * k + 2 * e + 1]));
-                                if (bad) {
-                                    const int r = half * 32 + k * 8 + 2 * (lane & 3);
-                                    const int from = G.from[q * 32 + g * 16 + 8 * e + (lane >> 2)];
-                                    if (rev ? r <= from : r >= from) o.x = __int_as_float(0x7fc00000);
-                                    if (rev ? r + 1 <= from : r + 1 >= from) o.y = __int_as_float(0x7fc00000);
-                                }
-                                pk[2 * k + e] = pack_bf16(o.x, o.y);
+                        for (int k = 0; k < 2; ++k)
+                            ldmatrix_x4_trans(zaddr + s * STAGE + k * 2048 + (g ? zstep : 0), z[g] + 4 * k);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) most = max_abs2(most, max_abs2(z[0][e], z[1][e]));
+                }
+                if (pass) break;
+                clean = group_sync_and(1, ZT, (most & 0x7fffu) < 0x7f80u && (most & 0x7fff0000u) < 0x7f800000u);
+                if (t == 0) G.bad = !clean;
+                if (clean) break;
+                if (t < 128) {
+                    int from = rev ? -1 : C;
+                    if (t < DZ) {
+#pragma unroll 1
+                        for (int x = 0; x < C; ++x) {
+                            const int r = rev ? x : C - 1 - x;   // the last write is the first token in time
+                            uint8_t *at = st + 2 * TILE + (t >> 6) * 8192 + r * 128 + (((t & 63) * 2) ^ ((r & 7) << 4));
+                            unsigned short &w = *reinterpret_cast<unsigned short *>(at);
+                            if ((w & 0x7f80u) == 0x7f80u) {
+                                w = 0;
+                                from = r;
                             }
                         }
-                        // matrices: channels +0 / +8 of token group k, then of k + 1
-                        const uint32_t to = stage + (half * 32 + (lane >> 4) * 8 + (lane & 7)) * RS +
-                                            (q * 32 + g * 16 + ((lane >> 3) & 1) * 8) * 2;
-                        stmatrix_x4_trans(to, pk[0], pk[1], pk[2], pk[3]);
-                        stmatrix_x4_trans(to + 16 * RS, pk[4], pk[5], pk[6], pk[7]);
+                    }
+                    G.from[t] = (short)from;
+                }
+                group_sync(1, ZT);   // once more, without them
+            }
+            if (i > 0) ok = wait(bar + B_KVF, (i - 1) & 1, s_abort);   // KV_{i-1} has read the parts
+            if (!G.narrow) {   // w_r goes to X, which QK_i has read
+                ok = ok && wait(bar + B_QKF, i & 1, s_abort);
+#pragma unroll 1
+                for (int e = t; e < C * DX / 8; e += ZT) {
+                    uint32_t *x = reinterpret_cast<uint32_t *>(st + e * 16);
+                    const float w = G.w[(e & 511) >> 3];
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) {
+                        const float2 v = __fmul2_rn(unpack(x[y]), make_float2(w, w));
+                        x[y] = pack_bf16(v.x, v.y);
                     }
                 }
                 fence_async_smem();
-                group_sync(2, 128);
-                const int r = q * 16 + lane;
-                if (lane < 16 && r < nv)
-                    bulk_store((TOut *)a.out + ((size_t)row0 + t0 + r) * ld + (size_t)h * DZ, sm + s * STAGE + r * RS, DZ * 2);
-                bulk_commit();
-                bulk_wait_read();
-                warp_arrive(bar + B_EMPTY + s);
             }
-            bulk_wait_all();
-        } else if ((warp & 3) < JW) {
-            const int j = (warp & 3) * 32 + lane;
-            for (int i = 0; i < nch; ++i) {
-                const int s = i % NS, t0 = chunk(i) * C;
-                if (!wait(bar + B_OF + i % NB, par(i), s_abort)) break;
+            if (!ok) continue;
+            if (q < JW) {
                 tc_fence_after();
-                const GateStage &G = gates[s];
-                const int nv = G.nv;
-                const bool bad = G.bad != 0;
-                const int from = bad ? G.from[j] : 0;
-                TOut *o = (TOut *)a.out + ((size_t)row0 + t0) * ld + (size_t)h * DZ + j;
 #pragma unroll 1
-                for (int blk = 0; blk < 4; ++blk, o += 16 * ld) {
-                    float u[16], v[16];
-                    tmem_ld16(tlane + TM_INTER + blk * 16, u);
-                    tmem_ld16(tlane + TM_INTRA + blk * 16, v);
-                    tmem_wait_ld();
+                for (int g = 0; g < 2; ++g) {
+                    uint32_t part[3][8];
 #pragma unroll
-                    for (int e = 0; e < 16; e += 4) {
-                        const float4 w = *reinterpret_cast<const float4 *>(&G.w_in[blk * 16 + e]);
-                        v[e] = fmaf(w.x, u[e], v[e]);
-                        v[e + 1] = fmaf(w.y, u[e + 1], v[e + 1]);
-                        v[e + 2] = fmaf(w.z, u[e + 2], v[e + 2]);
-                        v[e + 3] = fmaf(w.w, u[e + 3], v[e + 3]);
+                    for (int k = 0; k < 8; k += 2) {   // 8 tokens: u[k] channel lane/4, u[k+1] channel lane/4 + 8
+                        const float2 u = *reinterpret_cast<const float2 *>(&G.u[part0 * 2 + 4 * k + 2 * (lane & 3)]);
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            float2 x = __fmul2_rn(unpack(g ? z[1][k + e] : z[0][k + e]), u);
+                            part[0][k + e] = take_part(x);
+                            part[1][k + e] = take_part(x);
+                            part[2][k + e] = pack_bf16(x.x, x.y);
+                        }
                     }
-                    if (blk == 3) {   // the accumulators and this stage are read
+#pragma unroll
+                    for (int p = 0; p < 3; ++p)
+                        tmem_st_frag4(tlane + ((uint32_t)(g * 16) << 16) + TM_ZP + p * 32 + part0, part[p]);
+                }
+                tmem_wait_st();
+                tc_fence_before();
+            }
+            warp_arrive(bar + B_KBF);
+            // Z^T itself: O_{i-1} has read the last one
+            if (i > 0) ok = ok && wait(bar + B_OF + ((i - 1) & 1), ((i - 1) >> 1) & 1, s_abort);
+            if (!ok) continue;
+            if (q < JW) {
+                tc_fence_after();
+#pragma unroll
+                for (int g = 0; g < 2; ++g) tmem_st_frag4(tlane + ((uint32_t)(g * 16) << 16) + TM_Z + part0, z[g]);
+                tmem_wait_st();
+                tc_fence_before();
+            }
+            warp_arrive(bar + B_ZF);
+        }
+    } else if (wg == 3) {
+        regs_dec<RG_OUT>();
+        // ---- outputs: fragments of O^T (channel, token pair) go transposed into [token][channel] panels over
+        // this stage's X, which nobody reads any more, and leave from there by TMA (the last, ragged chunk of
+        // a sequence row by row: what lies behind it is another sequence's)
+        const size_t ld = (size_t)a.H * DZ;
+        const int q = warp & 3;
+        bool ok = true;
+        for (int i = 0; i < nch; ++i) {
+            const int s = i % NS, t0 = chunk(i) * C;
+            ok = wait(bar + B_OF + (i & 1), (i >> 1) & 1, s_abort);
+            if (!group_sync_and(2, 128, ok)) break;
+            tc_fence_after();
+            const GateStage &G = gates[s];
+            const int nv = G.nv;
+            const bool bad = G.bad != 0, narrow = G.narrow != 0;
+            if (q < JW) {
+                const int r0 = (lane >> 4) * 8 + (lane & 7), c0 = (q & 1) * 4 + ((lane >> 3) & 1);
+                const uint32_t rows = sb + s * STAGE + (q >> 1) * 8192 + r0 * 128;
+#pragma unroll 1
+                for (int x = 0; x < 4; ++x) {
+                    const int half = x >> 1, g = x & 1;   // 32 tokens, 16 channels
+                    float2 v[8];
+                    tmem_ld_frag4(tlane + ((uint32_t)(g * 16) << 16) + TM_O + half * 32, &v[0].x);
+                    tmem_wait_ld();
+                    if (x == 3) {   // the accumulator is read
                         tc_fence_before();
                         warp_arrive(bar + B_OE);
-                        warp_arrive(bar + B_EMPTY + s);
                     }
-                    TOut *at = o;
+                    if (narrow) {
 #pragma unroll
-                    for (int e = 0; e < 16; ++e, at += ld) {
-                        const int r = blk * 16 + e;
-                        if (bad && (rev ? r <= from : r >= from)) v[e] = __int_as_float(0x7fc00000);
-                        if (r < nv) st_out(at, v[e]);
+                        for (int k = 0; k < 4; ++k) {
+                            const float2 w = *reinterpret_cast<const float2 *>(&G.w[half * 32 + k * 8 + 2 * (lane & 3)]);
+                            v[2 * k] = __fmul2_rn(v[2 * k], w);
+                            v[2 * k + 1] = __fmul2_rn(v[2 * k + 1], w);
+                        }
                     }
+                    if (bad) {
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            const int r = half * 32 + (k >> 1) * 8 + 2 * (lane & 3);
+                            const int from = G.from[q * 32 + g * 16 + 8 * (k & 1) + (lane >> 2)];
+                            if (rev ? r <= from : r >= from) v[k].x = __int_as_float(0x7fc00000);
+                            if (rev ? r + 1 <= from : r + 1 >= from) v[k].y = __int_as_float(0x7fc00000);
+                        }
+                    }
+                    uint32_t pk[8];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) pk[k] = pack_bf16(v[k].x, v[k].y);
+                    // matrices: channels +0 / +8 of token group k, then of k + 1
+                    const uint32_t to = rows + half * 4096 + (((c0 + g * 2) ^ (r0 & 7)) << 4);
+                    stmatrix_x4_trans(to, pk[0], pk[1], pk[2], pk[3]);
+                    stmatrix_x4_trans(to + 2048, pk[4], pk[5], pk[6], pk[7]);
                 }
             }
+            fence_async_smem();
+            group_sync(2, 128);
+            if (nv == C) {
+                if (tid == 3 * 128) {
+#pragma unroll
+                    for (int p = 0; p < DZ / 64; ++p)
+                        tma_store_3d(&P.to, sm + s * STAGE + p * 8192, p * 64, h, row0 + t0);
+                    bulk_commit();
+                    bulk_wait_read();
+                }
+            } else {
+                __nv_bfloat16 *o = (__nv_bfloat16 *)a.out + ((size_t)row0 + t0) * ld + (size_t)h * DZ;
+#pragma unroll 1
+                for (int e = tid - 3 * 128; e < nv * (DZ / 8); e += 128) {
+                    const int r = e / (DZ / 8), ch = e % (DZ / 8);
+                    *reinterpret_cast<uint4 *>(o + r * ld + ch * 8) = *reinterpret_cast<const uint4 *>(
+                        sm + s * STAGE + (ch >> 3) * 8192 + r * 128 + (((ch & 7) ^ (r & 7)) << 4));
+                }
+            }
+            warp_arrive(bar + B_EMPTY + s);
         }
+        bulk_wait_all();
     } else {
         regs_inc<RG_STATE>();
         // ---- state: row j of R^T, half of its columns
@@ -634,42 +554,43 @@ __global__ void __launch_bounds__(NT, 1) lin_chunk_kernel(const __grid_constant_
             bool ok = true;
             // iteration i: the state before it is published (and written where it is a boundary's or the last)
             for (int i = 0;; ++i) {
-                float *to[2] = {nullptr, nullptr};
-                // the token whose boundary this state is: backward the chunk to come ends there, forward the last one did
-                const int edge = rev ? (i < nch ? min(len, (chunk(i) + 1) * C) - 1 : -1) : min(len, i * C) - 1;
-                if (a.snap && edge >= 0 && (edge == len - 1 || (edge + 1) % a.snap_tokens == 0))
-                    to[0] = a.snap + ((size_t)(n + row0 / a.snap_tokens + edge / a.snap_tokens) * a.H + h) * DX * DZ;
-                if (i == nch && a.s_out) to[1] = a.s_out + soff;
+                if (a.snap || i == nch) {
+                    float *to[2] = {nullptr, nullptr};
+                    // the token whose boundary this state is: backward the chunk to come ends there, forward the
+                    // last one did
+                    const int edge = rev ? (i < nch ? min(len, (chunk(i) + 1) * C) - 1 : -1) : min(len, i * C) - 1;
+                    if (a.snap && edge >= 0 && (edge == len - 1 || (edge + 1) % a.snap_tokens == 0))
+                        to[0] = a.snap + ((size_t)(n + row0 / a.snap_tokens + edge / a.snap_tokens) * a.H + h) * DX * DZ;
+                    if (i == nch && a.s_out) to[1] = a.s_out + soff;
 #pragma unroll 1
-                for (int w = 0; w < 2; ++w) {
-                    float *dst = w ? to[1] : to[0];
-                    if (!dst) continue;
-                    dst += (size_t)i0 * DZ + j;
+                    for (int w = 0; w < 2; ++w) {
+                        float *dst = w ? to[1] : to[0];
+                        if (!dst) continue;
+                        dst += (size_t)i0 * DZ + j;
 #pragma unroll
-                    for (int e = 0; e < CX / 2; ++e) {
-                        dst[2 * e * DZ] = S[e].x;
-                        dst[(2 * e + 1) * DZ] = S[e].y;
+                        for (int e = 0; e < CX / 2; ++e) {
+                            dst[2 * e * DZ] = S[e].x;
+                            dst[(2 * e + 1) * DZ] = S[e].y;
+                        }
                     }
+                    if (i == nch) break;
                 }
-                if (i == nch) break;
                 if (i > 0) {
-                    ok = wait(bar + B_SE, (i - 1) & 1, s_abort);   // inter_{i-1} has read the parts
+                    ok = wait(bar + B_SE, (i - 1) & 1, s_abort);   // O_{i-1} has read the parts
                     if (!ok) break;
                     tc_fence_after();
                 }
-                // the bf16 parts of the state, for `inter`
 #pragma unroll
                 for (int b = 0; b < CX / 16; ++b) {
-                    uint32_t part[NSP][8];
+                    uint32_t hi[8], lo[8];
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
                         float2 x = S[b * 8 + e];
-#pragma unroll
-                        for (int p = 0; p < NSP - 1; ++p) part[p][e] = take_part(x);
-                        part[NSP - 1][e] = pack_bf16(x.x, x.y);
+                        hi[e] = take_part(x);
+                        lo[e] = pack_bf16(x.x, x.y);
                     }
-#pragma unroll
-                    for (int p = 0; p < NSP; ++p) tmem_st8(tlane + TM_S + p * 64 + i0 / 2 + b * 8, part[p]);
+                    tmem_st8(tlane + TM_S + i0 / 2 + b * 8, hi);
+                    tmem_st8(tlane + TM_S + 64 + i0 / 2 + b * 8, lo);
                 }
                 tmem_wait_st();
                 tc_fence_before();
@@ -708,71 +629,19 @@ __global__ void __launch_bounds__(NT, 1) lin_chunk_kernel(const __grid_constant_
     if (tid == 0 && *s_abort) atomicOr(P.status, DEV_WAIT_TIMEOUT);
 }
 
-// ---- host side --------------------------------------------------------------
-typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
-                                  const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn()
-{
-    static EncodeTiledFn fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void *p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<EncodeTiledFn>(p);
-    });
-    return fn;
-}
-
-// [rows][heads][d] bf16; box of 64 channels of one head, 64 rows, 128-byte swizzle (one operand panel)
-bool make_map(CUtensorMap *m, const void *base, long long rows, int heads, int d)
-{
-    cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)rows};
-    cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)heads * d * 2};
-    cuuint32_t box[3] = {64, 1, 64}, es[3] = {1, 1, 1};
-    EncodeTiledFn fn = encode_fn();
-    if (!fn) return false;
-    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, es,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// Per-device one-time set-up of a kernel: its dynamic shared memory.
-template <typename K> cudaError_t opt_in(K kernel, uint32_t bytes, bool (&done)[64])
-{
-    static std::mutex mu;
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-    // makes the device's context the thread's current one, which encoding a tensor map needs: a thread
-    // that has made no runtime call yet (autograd's) has none
-    if ((e = cudaSetDevice(dev)) != cudaSuccess) return e;
-    std::lock_guard<std::mutex> lock(mu);
-    if (!done[dev]) {
-        if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) != cudaSuccess) return e;
-        done[dev] = true;
-    }
-    return cudaSuccess;
-}
-
-template <int DX, int DZ, int NSP, int NPP, typename TOut> cudaError_t launch_dims(const LinRun &r, cudaStream_t st)
+template <int DX, int DZ> cudaError_t launch_dims(const LinRun &r, cudaStream_t st)
 {
     static bool done[64] = {};
-    cudaError_t e = opt_in(lin_chunk_kernel<DX, DZ, NSP, NPP, TOut>, SM_ALLOC, done);
+    cudaError_t e = opt_in(lin_chunk_kernel<DX, DZ>, SM_ALLOC, done);
     if (e != cudaSuccess) return e;
     LinChunkParams p;
     memset(&p, 0, sizeof(p));
     p.a = r;
     if ((e = device_status_word(&p.status)) != cudaSuccess) return e;
-    const long long rows = r.rows;
-    if (rows > 0 && (!make_map(&p.tx, r.x, rows, r.H / r.gx, DX) || !make_map(&p.ty, r.y, rows, r.H / r.gy, DX) ||
-                     !make_map(&p.tz, r.z, rows, r.H / r.gz, DZ)))
+    if (r.rows > 0 && (!make_map(&p.tx, r.x, r.rows, r.H / r.gx, DX) || !make_map(&p.ty, r.y, r.rows, r.H / r.gy, DX) ||
+                       !make_map(&p.tz, r.z, r.rows, r.H / r.gz, DZ) || !make_map(&p.to, r.out, r.rows, r.H, DZ)))
         return cudaErrorInvalidValue;
-    lin_chunk_kernel<DX, DZ, NSP, NPP, TOut><<<(unsigned)(r.num_seqs * r.H), NT, SM_ALLOC, st>>>(p);
+    lin_chunk_kernel<DX, DZ><<<(unsigned)(r.num_seqs * r.H), NT, SM_ALLOC, st>>>(p);
     return cudaGetLastError();
 }
 
@@ -782,11 +651,10 @@ bool lin_chunk_takes(int dx, int dz) { return (dx == 64 || dx == 128) && (dz == 
 
 cudaError_t launch_lin_chunk(const LinRun &r, int dx, int dz, cudaStream_t st)
 {
-    const bool fine = r.out_f32 != 0;
-    if (dx == 128 && dz == 128) return fine ? launch_dims<128, 128, 3, 2, float>(r, st) : launch_dims<128, 128, 2, 1, __nv_bfloat16>(r, st);
-    if (dx == 128 && dz == 64) return fine ? launch_dims<128, 64, 3, 2, float>(r, st) : launch_dims<128, 64, 2, 1, __nv_bfloat16>(r, st);
-    if (dx == 64 && dz == 128) return fine ? launch_dims<64, 128, 3, 2, float>(r, st) : launch_dims<64, 128, 2, 1, __nv_bfloat16>(r, st);
-    if (dx == 64 && dz == 64) return fine ? launch_dims<64, 64, 3, 2, float>(r, st) : launch_dims<64, 64, 2, 1, __nv_bfloat16>(r, st);
+    if (dx == 128 && dz == 128) return launch_dims<128, 128>(r, st);
+    if (dx == 128 && dz == 64) return launch_dims<128, 64>(r, st);
+    if (dx == 64 && dz == 128) return launch_dims<64, 128>(r, st);
+    if (dx == 64 && dz == 64) return launch_dims<64, 64>(r, st);
     return cudaErrorInvalidValue;
 }
 

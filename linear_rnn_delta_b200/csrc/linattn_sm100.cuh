@@ -1,0 +1,149 @@
+// Shared parts of linear attention's tensor-core kernels: waits, fixed-point decays, tensor maps.
+#pragma once
+
+#include <cuda.h>
+#include <mutex>
+#include <cstring>
+
+#include "common.cuh"
+#include "linattn.cuh"
+#include "sm100.cuh"
+
+namespace kda {
+namespace lin {
+
+using namespace sm100;
+
+constexpr int C = 64;                                 // tokens of a chunk
+constexpr uint32_t TILE = 16384;                      // [64 tokens][128 channels] bf16: two panels of 64 channels
+constexpr uint32_t STAGE = 3 * TILE;                  // X, Y, Z
+
+constexpr long long WAIT_LIMIT = 1ll << 32;           // cycles, about 2 s (the last waits of a CTA)
+constexpr uint32_t WAIT_NS = 1000000, WAIT_POLLS = 2000;   // a poll sleeps for up to 1 ms: about 2 s
+constexpr unsigned DEV_WAIT_TIMEOUT = 1u;
+
+// Descriptors (low words): K step kk of a K-major tile in panels of 64 elements, and of an MN-major
+// [token][channel] tile in panels of 64 channels; `base` the tile's own.
+__device__ __forceinline__ uint32_t k_tile(uint32_t saddr) { return desc_sw128_lo(saddr, 16); }
+__device__ __forceinline__ uint32_t dK(uint32_t base, int kk) { return base + (uint32_t)((kk >> 2) * 512 + (kk & 3) * 2); }
+__device__ __forceinline__ uint32_t mn_tile(uint32_t saddr) { return desc_sw128_lo(saddr, 8192); }
+__device__ __forceinline__ uint32_t dMN(uint32_t base, int kk) { return base + (uint32_t)(kk * 128); }
+
+// Waits for a phase; false if the wait ran out here (recorded for the others) or elsewhere.  A warp has one
+// answer.
+__device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, volatile int *abort)
+{
+    uint32_t polls = 0;
+    while (!__all_sync(0xffffffffu, mbar_try_wait_ns(bar, parity, WAIT_NS) != 0)) {
+        if (__any_sync(0xffffffffu, *abort != 0) || ++polls > WAIT_POLLS) {
+            *abort = 1;
+            return false;
+        }
+    }
+    return true;
+}
+__device__ __forceinline__ void warp_arrive(uint64_t *bar)   // one arrival for the warp, behind all its lanes
+{
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+}
+
+__device__ __forceinline__ float2 unpack(uint32_t w)
+{
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+// next bf16 part of a pair: rounds x, leaves the rest in x
+__device__ __forceinline__ uint32_t take_part(float2 &x)
+{
+    const uint32_t w = pack_bf16(x.x, x.y);
+    x = __ffma2_rn(unpack(w), make_float2(-1.f, -1.f), x);
+    return w;
+}
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// Log2-decays are summed as 64-bit fixed point with 32 bits behind the point: sums and differences are exact,
+// a term is off by 2^-33.
+__device__ __forceinline__ long long fix_log2(float g)
+{
+    // g log2(e) as two floats: the rounding of the product, and of log2(e), would show in long sums
+    const float hi = g * 1.44269502f, lo = fmaf(g, 1.44269502f, -hi) + g * 1.92596303e-8f;
+    const float n = rintf(hi);
+    return ((long long)(int)n << 32) + (long long)__float2ll_rn(((hi - n) + lo) * 4294967296.f);
+}
+// integer part and rest in [-1/2, 1/2)
+__device__ __forceinline__ int fix_int(long long x) { return (int)((x + 0x80000000ll) >> 32); }
+__device__ __forceinline__ float fix_rest(long long x) { return (float)(int)(unsigned)x * 2.3283064365386963e-10f; }
+// 2^x, its error that of the rest's exponential whatever the size of x; below 2^-126 it is 0
+__device__ __forceinline__ float fix_exp2(long long x)
+{
+    const int n = fix_int(x);
+    const float by = n < -126 ? 0.f : __int_as_float(n > 127 ? 0x7f800000 : (n + 127) << 23);
+    return ex2(fix_rest(x)) * by;
+}
+__device__ __forceinline__ float diff(float2 a, float2 b) { return (a.x - b.x) + (a.y - b.y); }
+
+// max of the magnitudes of two bf16 pairs, NaN if either is one
+__device__ __forceinline__ uint32_t max_abs2(uint32_t x, uint32_t y)
+{
+    uint32_t r;
+    asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
+    return r;
+}
+
+// ---- host side --------------------------------------------------------------
+typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                  const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+inline EncodeTiledFn encode_fn()
+{
+    static EncodeTiledFn fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<EncodeTiledFn>(p);
+    });
+    return fn;
+}
+
+// [rows][heads][d] bf16; box of 64 channels of one head, 64 rows, 128-byte swizzle (one operand panel)
+inline bool make_map(CUtensorMap *m, const void *base, long long rows, int heads, int d)
+{
+    cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)rows};
+    cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)heads * d * 2};
+    cuuint32_t box[3] = {64, 1, 64}, es[3] = {1, 1, 1};
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, es,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Per-device one-time set-up of a kernel: its dynamic shared memory.
+template <typename K> cudaError_t opt_in(K kernel, uint32_t bytes, bool (&done)[64])
+{
+    static std::mutex mu;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    // makes the device's context the thread's current one, which encoding a tensor map needs: a thread
+    // that has made no runtime call yet (autograd's) has none
+    if ((e = cudaSetDevice(dev)) != cudaSuccess) return e;
+    std::lock_guard<std::mutex> lock(mu);
+    if (!done[dev]) {
+        if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) != cudaSuccess) return e;
+        done[dev] = true;
+    }
+    return cudaSuccess;
+}
+
+}  // namespace lin
+}  // namespace kda

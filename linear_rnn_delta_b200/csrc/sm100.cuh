@@ -82,15 +82,48 @@ __device__ __forceinline__ void mma_bf16(uint32_t d_tmem, uint64_t adesc, uint64
         :: "r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate) : "memory");
 }
 
-// A from tensor memory (lane = M row, two consecutive K elements in a column)
-__device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
-                                            uint32_t accumulate)
+// ---- MMA issue by a whole warp ---------------------------------------------
+// In uniform control flow, issued by the lane with `leader` set (the same one throughout, commits included).
+// Branching to one thread first costs each MMA its operands' way into uniform registers: 57 cycles an MMA,
+// against 32 for a 128x64x16 product (A in tensor memory).  For the same reason a descriptor comes as its low
+// word, in which a K step is an addition of a constant, and a high word that is one.
+constexpr uint32_t DESC_SW128_HI = (1024u >> 4) | (1u << 14) | (2u << 29);   // SBO 1024, version 1, 128-byte swizzle
+__device__ __forceinline__ uint32_t desc_sw128_lo(uint32_t saddr, uint32_t lbo)
+{
+    return ((saddr >> 4) & 0x3FFFu) | ((lbo >> 4) << 16);
+}
+__device__ __forceinline__ void mma_bf16_warp(uint32_t d_tmem, uint32_t adesc_lo, uint32_t bdesc_lo, uint32_t idesc,
+                                              uint32_t accumulate, uint32_t leader)
 {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 a, b;\n\t"
+        "mov.b64 a, {%1, %6};\n\tmov.b64 b, {%2, %6};\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
-        :: "r"(d_tmem), "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate) : "memory");
+        "setp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}"
+        :: "r"(d_tmem), "r"(adesc_lo), "r"(bdesc_lo), "r"(idesc), "r"(accumulate), "r"(leader), "n"(DESC_SW128_HI)
+        : "memory");
+}
+// A from tensor memory (lane = M row, two consecutive K elements in a column)
+__device__ __forceinline__ void mma_bf16_ts_warp(uint32_t d_tmem, uint32_t a_tmem, uint32_t bdesc_lo, uint32_t idesc,
+                                                 uint32_t accumulate, uint32_t leader)
+{
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 b;\n\t"
+        "mov.b64 b, {%2, %6};\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "setp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}"
+        :: "r"(d_tmem), "r"(a_tmem), "r"(bdesc_lo), "r"(idesc), "r"(accumulate), "r"(leader), "n"(DESC_SW128_HI)
+        : "memory");
+}
+__device__ __forceinline__ void mma_commit_warp(uint64_t *mbar, uint32_t leader)
+{
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "setp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}"
+        :: "r"(smem_u32(mbar)), "r"(leader) : "memory");
 }
 
 // Arrive on the mbarrier once every MMA issued so far by this thread completes.
@@ -118,6 +151,18 @@ __device__ __forceinline__ uint32_t mbar_try_wait(uint64_t *mbar, uint32_t parit
         "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
         "selp.u32 %0, 1, 0, p;\n\t}"
         : "=r"(ok) : "r"(smem_u32(mbar)), "r"(parity) : "memory");
+    return ok;
+}
+// The same, asleep for up to `ns` nanoseconds while the phase is not complete (a warp that polls takes issue
+// slots and shared-memory cycles from those that work).
+__device__ __forceinline__ uint32_t mbar_try_wait_ns(uint64_t *mbar, uint32_t parity, uint32_t ns)
+{
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok) : "r"(smem_u32(mbar)), "r"(parity), "r"(ns) : "memory");
     return ok;
 }
 // Bounded wait: returns false if the phase did not complete within
@@ -226,6 +271,30 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t *u)
                  :: "r"(taddr), "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7])
                  : "memory");
 }
+// 16 lanes x 32 columns from the fragments of eight 16x(4 columns) pieces: u[2k] is lane t/4, column 4k + t%4,
+// u[2k+1] the same column of lane t/4 + 8
+__device__ __forceinline__ void tmem_st_frag8(uint32_t taddr, const uint32_t *u)
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], "
+        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
+        :: "r"(taddr), "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7]),
+           "r"(u[8]), "r"(u[9]), "r"(u[10]), "r"(u[11]), "r"(u[12]), "r"(u[13]), "r"(u[14]), "r"(u[15])
+        : "memory");
+}
+// ... 16 columns, four pieces
+__device__ __forceinline__ void tmem_st_frag4(uint32_t taddr, const uint32_t *u)
+{
+    asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
+                 :: "r"(taddr), "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7])
+                 : "memory");
+}
+// four 8x8 matrices of 16-bit elements, transposed: lane l gives the address of row l%8 of matrix l/8
+__device__ __forceinline__ void ldmatrix_x4_trans(uint32_t saddr, uint32_t *u)
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]) : "r"(saddr) : "memory");
+}
 // four 8x8 matrices of 16-bit elements, stored transposed: lane l gives the address of row l%8 (a column of
 // the fragment) of matrix l/8
 __device__ __forceinline__ void stmatrix_x4_trans(uint32_t saddr, uint32_t a, uint32_t b, uint32_t c, uint32_t d)
@@ -261,6 +330,12 @@ __device__ __forceinline__ void bulk_store(void *gdst, const void *smem_src, uin
 {
     asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;"
                  :: "l"(gdst), "r"(smem_u32(smem_src)), "r"(bytes) : "memory");
+}
+// 3-D box from shared memory to the tensor map's tensor, in the issuing thread's bulk async-group
+__device__ __forceinline__ void tma_store_3d(const void *tmap, const void *smem_src, int c0, int c1, int c2)
+{
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];"
+                 :: "l"(tmap), "r"(smem_u32(smem_src)), "r"(c0), "r"(c1), "r"(c2) : "memory");
 }
 __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
 // the issuing thread's bulk stores have finished reading shared memory

@@ -5,7 +5,8 @@ magnitudes, plus half a step of its output type relative to itself (bf16 2^-8, f
   - the token scan rounds the state twice a token and adds d products: c = (2 T + d + 8) 2^-24;
   - the chunked form splits fp32 factors into bf16 parts.  Two parts leave 2^-16 of the value at most (a rounding
     is off by 2^-8 of the value, the second by 2^-8 of that): the state in o and dv.  The pairs' weights within a chunk are
-    rounded once in o and dv: 2^-8 of the sum over pairs of their magnitude, pair_size.  States, dq and dk have
+    rounded once in o and dv: 2^-8 of the sum over pairs of their magnitude, pair_size.  In a chunk that decays
+    by more than 2^-96 (`strong`) w_r x_r is rounded once instead, too: 2^-8 of A.  States, dq and dk have
     three parts (2^-24) and keep the scan's allowance: their own additions are fewer than the scan's.
 dq, dk that several heads share are sums over them (A is, too).  Gate gradients are sums of q.dq - k.dk, whose
 sizes gate_sum_size adds up.
@@ -65,12 +66,14 @@ def allowances(dtype, T, dk, dv):
     return scan, scan + (2.0 ** -16 if dtype == torch.bfloat16 else 0.0)
 
 
-def pairs(x, q, k, z, r, back=False):
-    """Allowance for the pairs' weights of the chunked form."""
-    return 2.0 ** -8 * ref.pair_size(q, k, z, r["g"], r["cu"], back) if x["q"].dtype == torch.bfloat16 else 0.0
+def pairs(x, q, k, z, r, mag, strong, back=False):
+    """Allowance for the weights that the chunked form rounds once."""
+    if x["q"].dtype != torch.bfloat16:
+        return 0.0
+    return 2.0 ** -8 * (ref.pair_size(q, k, z, r["g"], r["cu"], back) + (mag if strong else 0.0))
 
 
-def check_fwd(kda, x, flags=0, states=False):
+def check_fwd(kda, x, flags=0, states=False, strong=False):
     T, dk, dv = x["q"].shape[1], x["q"].shape[3], x["v"].shape[3]
     d, r = dev(x), f64(x)
     got = kda.kda_linattn_chunk_fwd(d["q"], d["k"], d["v"], d["g"], cu_seqlens=d["cu"], initial_state=d["s0"],
@@ -80,7 +83,7 @@ def check_fwd(kda, x, flags=0, states=False):
     mo, msf, mS = ref.forward(r["q"].abs(), r["k"].abs(), r["v"].abs(), r["g"], r["cu"],
                               None if r["s0"] is None else r["s0"].abs())
     c, co = allowances(x["q"].dtype, T, dk, dv)
-    near(got[0], o, mo + pairs(x, r["q"], r["k"], r["v"], r) / co, co, STEP[x["q"].dtype], "o")
+    near(got[0], o, mo + pairs(x, r["q"], r["k"], r["v"], r, mo, strong) / co, co, STEP[x["q"].dtype], "o")
     near(got[1], sf, msf, c, STEP[torch.float32], "final_state")
     if states:
         for n, (b, lo, hi) in enumerate(ref.spans(T, x["q"].shape[0], x["cu"])):
@@ -92,7 +95,7 @@ def check_fwd(kda, x, flags=0, states=False):
     return got
 
 
-def check_bwd(kda, x, flags=0):
+def check_bwd(kda, x, flags=0, strong=False):
     T, dk, dv = x["q"].shape[1], x["q"].shape[3], x["v"].shape[3]
     d, r = dev(x), f64(x)
     got = kda.kda_linattn_chunk_bwd(d["q"], d["k"], d["v"], d["g"], d["do"], d["dsf"], cu_seqlens=d["cu"],
@@ -110,7 +113,7 @@ def check_bwd(kda, x, flags=0):
     step = STEP[x["q"].dtype]
     near(got[0], want.dq, mag.dq, c, step, "dq")
     near(got[1], want.dk, mag.dk, c, step, "dk")
-    near(got[2], want.dv, mag.dv + pairs(x, r["q"], r["k"], r["do"], r, back=True) / co, co, step, "dv")
+    near(got[2], want.dv, mag.dv + pairs(x, r["q"], r["k"], r["do"], r, mag.dv, strong, back=True) / co, co, step, "dv")
     near(got[3], want.dg, size_g, c, STEP[torch.float32], "dg")
     near(got[4], want.ds0, mag.ds0, c, STEP[torch.float32], "d_initial_state")
     assert got[0].dtype == x["q"].dtype and got[3].dtype == torch.float32 and got[3].shape == x["g"].shape
@@ -201,9 +204,9 @@ def test_resets_and_extreme_decays(kda, dtype, d):
     g[0, 60:70] = -30.0
     g[0, 100] = -200.0
     g[0, 127:129] = -math.inf
-    got = check_fwd(kda, x, states=True)
+    got = check_fwd(kda, x, states=True, strong=True)
     assert torch.isfinite(got[0]).all()
-    dg = check_bwd(kda, x)[3]
+    dg = check_bwd(kda, x, strong=True)[3]
     assert (dg[0, [0, 10, 11, 127, 128]] == 0).all()
 
 
@@ -213,8 +216,8 @@ def test_no_decay_and_total_decay(kda):
     for g in (0.0, -math.inf):
         x = make(7, torch.bfloat16, 1, 200, 1, 1, 128, 128, init=True)
         x["g"] = torch.full_like(x["g"], g)
-        check_fwd(kda, x)
-        check_bwd(kda, x)
+        check_fwd(kda, x, strong=g < 0)
+        check_bwd(kda, x, strong=g < 0)
 
 
 @gpu
@@ -275,7 +278,7 @@ def test_prompt_then_decode_equals_one_sequence(kda, dtype):
     want, sf, _ = ref.forward(r["q"], r["k"], r["v"], r["g"])
     mo, msf, _ = ref.forward(r["q"].abs(), r["k"].abs(), r["v"].abs(), r["g"])
     c, co = allowances(DT[dtype], 140, 64, 128)
-    near(got, want, mo + pairs(x, r["q"], r["k"], r["v"], r) / co, co, STEP[DT[dtype]], "o")
+    near(got, want, mo + pairs(x, r["q"], r["k"], r["v"], r, mo, False) / co, co, STEP[DT[dtype]], "o")
     near(state, sf, msf, c, 2.0 ** -24, "state")
 
 
