@@ -488,23 +488,36 @@ def kda_decode_step(variant: Union[str, int], gate_range: Union[str, int], q: to
     return o
 
 
-def _lin_inputs(q, k, v, g, packed):
+# The calls below are made once a token and layer in a decode loop, so what they check is checked in a few
+# comparisons; a mismatch goes to _check for its words.
+def _fits(t: torch.Tensor, name: str, dtype, shape, device):
+    if t.dtype is not dtype or t.shape != shape or t.device != device or not t.is_contiguous() or not t.is_cuda:
+        _check(t, name, dtype, shape, device)
+
+
+def _fits_opt(t: Optional[torch.Tensor], name: str, dtype, shape, device):
+    if t is not None:
+        _fits(t, name, dtype, shape, device)
+
+
+def _lin_inputs(q, k, v, g, sequences):
     """Shapes of linear attention's inputs ([B,T,heads,d], or [N,heads,d] for a decode step), checked."""
-    lead = 2 if packed else 1
-    if q.dim() != lead + 2 or v.dim() != lead + 2:
-        raise ValueError("q, k must be [B,T,Hk,d_k] and v [B,T,H,d_v]" if packed else
+    qs, vs = q.shape, v.shape
+    dims = 4 if sequences else 3
+    if len(qs) != dims or len(vs) != dims:
+        raise ValueError("q, k must be [B,T,Hk,d_k] and v [B,T,H,d_v]" if sequences else
                          "q, k must be [N,Hk,d_k] and v [N,H,d_v]")
     dt, dev = q.dtype, q.device
     if dt not in _DTYPES:
         raise ValueError(f"dtype {dt} unsupported (bf16 or fp32)")
-    (Hk, dk), (H, dv) = q.shape[lead:], v.shape[lead:]
+    lead, (Hk, dk), (H, dv) = qs[:-2], qs[-2:], vs[-2:]
     if Hk < 1 or H % Hk:
         raise ValueError(f"{H} value heads are not a multiple of {Hk} query and key heads")
-    _check(q, "q", dt, q.shape, dev)
-    _check(k, "k", dt, q.shape, dev)
-    _check(v, "v", dt, (*q.shape[:lead], H, dv), dev)
+    _fits(q, "q", dt, qs, dev)
+    _fits(k, "k", dt, qs, dev)
+    _fits(v, "v", dt, (*lead, H, dv), dev)
     per_token = g.dim() != 1
-    _check(g, "g", torch.float32, (*q.shape[:lead], H) if per_token else (H,), dev)
+    _fits(g, "g", torch.float32, (*lead, H) if per_token else (H,), dev)
     return dt, dev, Hk, H, dk, dv, int(per_token)
 
 
@@ -513,16 +526,42 @@ def _num_seqs(cu_seqlens, B, dev):
         return B
     if cu_seqlens.dtype != torch.int32 or not cu_seqlens.is_cuda or cu_seqlens.dim() != 1:
         raise ValueError("cu_seqlens must be a 1-D int32 CUDA tensor")
-    _check(cu_seqlens, "cu_seqlens", torch.int32, cu_seqlens.shape, dev)
+    _fits(cu_seqlens, "cu_seqlens", torch.int32, cu_seqlens.shape, dev)
     return cu_seqlens.numel() - 1
+
+
+class _Here:
+    """Nothing to enter: the tensors' device is the current one, and so is the stream."""
+
+    def __enter__(self):
+        return None
+
+    def __exit__(self, *_):
+        return False
+
+
+_HERE = _Here()
 
 
 def _launching(stream, dev):
     """Context in which a call allocates and launches: the tensors' device, and the memory pool of the stream
     that the kernels run on (what torch hands out is then free on that stream)."""
     if stream is None:
-        return torch.cuda.device(dev)
-    return torch.cuda.stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream), dev))
+        return _HERE if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), dev)
+    if stream.device != dev:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
+    return torch.cuda.stream(stream)
+
+
+def _raw_stream(dev):
+    """The current stream of the (current) device, which _launching has made the launching one."""
+    return torch._C._cuda_getCurrentRawStream(dev.index)
+
+
+def _at(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
 
 
 def kda_linattn_chunk_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor,
@@ -543,7 +582,7 @@ def kda_linattn_chunk_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: 
     f32 = dict(dtype=torch.float32, device=dev)
     states, snaps = (N, H, dk, dv), (num_chunk_slots(B, T, N), H, dk, dv)
     want_states = chunk_states is not None and chunk_states is not False
-    _check(initial_state, "initial_state", torch.float32, states, dev)
+    _fits_opt(initial_state, "initial_state", torch.float32, states, dev)
     sizes = (_DTYPES[dt], B, T, Hk, H, dk, dv)
     with _launching(stream, dev):
         if final_state is True:
@@ -556,14 +595,14 @@ def kda_linattn_chunk_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: 
             chunk_states = None
         if o is None:
             o = torch.empty((B, T, H, dv), dtype=dt, device=dev)
-        _check(final_state, "final_state", torch.float32, states, dev)
-        _check(o, "o", dt, (B, T, H, dv), dev)
-        _check(chunk_states, "chunk_states", torch.float32, snaps, dev)
+        _fits_opt(final_state, "final_state", torch.float32, states, dev)
+        _fits_opt(o, "o", dt, (B, T, H, dv), dev)
+        _fits_opt(chunk_states, "chunk_states", torch.float32, snaps, dev)
         ws_bytes = lib.kda_linattn_chunk_fwd_workspace_size(*sizes, int(cu_seqlens is not None), N, int(flags))
         ws = torch.empty(ws_bytes, dtype=torch.uint8, device=dev) if ws_bytes else None
-        rc = lib.kda_linattn_chunk_fwd(*sizes, _ptr(q), _ptr(k), _ptr(v), _ptr(g), per_token, _ptr(cu_seqlens), N,
-                                       _ptr(initial_state), _ptr(final_state), _ptr(chunk_states), _ptr(o), _ptr(ws),
-                                       ws_bytes, int(flags), _stream(stream, dev))
+        rc = lib.kda_linattn_chunk_fwd(*sizes, _at(q), _at(k), _at(v), _at(g), per_token, _at(cu_seqlens), N,
+                                       _at(initial_state), _at(final_state), _at(chunk_states), _at(o), _at(ws),
+                                       ws_bytes, int(flags), _raw_stream(dev))
     if rc != 0:
         raise KdaError(rc, "kda_linattn_chunk_fwd")
     if want_states:
@@ -583,10 +622,10 @@ def kda_linattn_chunk_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: 
     fp32 (None unless ``d_initial_state``)."""
     dt, dev, Hk, H, dk, dv, per_token = _lin_inputs(q, k, v, g, True)
     B, T = q.shape[:2]
-    _check(d_o, "d_o", dt, v.shape, dev)
+    _fits_opt(d_o, "d_o", dt, v.shape, dev)
     N = _num_seqs(cu_seqlens, B, dev)
-    _check(initial_state, "initial_state", torch.float32, (N, H, dk, dv), dev)
-    _check(d_final_state, "d_final_state", torch.float32, (N, H, dk, dv), dev)
+    _fits_opt(initial_state, "initial_state", torch.float32, (N, H, dk, dv), dev)
+    _fits_opt(d_final_state, "d_final_state", torch.float32, (N, H, dk, dv), dev)
     sizes = (_DTYPES[dt], B, T, Hk, H, dk, dv)
     with _launching(stream, dev):
         dqt, dkt, dvt, dgt = (torch.empty_like(x) for x in (q, k, v, g))
@@ -595,10 +634,10 @@ def kda_linattn_chunk_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: 
         if ws_bytes == 0:
             raise KdaError(1, "kda_linattn_chunk_bwd_workspace_size")
         ws = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
-        rc = lib.kda_linattn_chunk_bwd(*sizes, _ptr(q), _ptr(k), _ptr(v), _ptr(g), per_token, _ptr(cu_seqlens), N,
-                                       _ptr(initial_state), _ptr(d_o), _ptr(d_final_state), _ptr(dqt), _ptr(dkt),
-                                       _ptr(dvt), _ptr(dgt), _ptr(ds0), _ptr(ws), ws_bytes, int(flags),
-                                       _stream(stream, dev))
+        rc = lib.kda_linattn_chunk_bwd(*sizes, _at(q), _at(k), _at(v), _at(g), per_token, _at(cu_seqlens), N,
+                                       _at(initial_state), _at(d_o), _at(d_final_state), _at(dqt), _at(dkt),
+                                       _at(dvt), _at(dgt), _at(ds0), _at(ws), ws_bytes, int(flags),
+                                       _raw_stream(dev))
     if rc != 0:
         raise KdaError(rc, "kda_linattn_chunk_bwd")
     return dqt, dkt, dvt, dgt, ds0
@@ -634,13 +673,13 @@ def kda_linattn_decode_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g
     [N,H,d_v]."""
     dt, dev, Hk, H, dk, dv, per_token = _lin_inputs(q, k, v, g, False)
     N = q.shape[0]
-    _check(state, "state", torch.float32, (N, H, dk, dv), dev)
+    _fits_opt(state, "state", torch.float32, (N, H, dk, dv), dev)
     with _launching(stream, dev):
         if o is None:
             o = torch.empty((N, H, dv), dtype=dt, device=dev)
-        _check(o, "o", dt, (N, H, dv), dev)
-        rc = lib.kda_linattn_decode_step(_DTYPES[dt], N, Hk, H, dk, dv, _ptr(q), _ptr(k), _ptr(v), _ptr(g), per_token,
-                                         _ptr(state), _ptr(o), int(flags), _stream(stream, dev))
+        _fits_opt(o, "o", dt, (N, H, dv), dev)
+        rc = lib.kda_linattn_decode_step(_DTYPES[dt], N, Hk, H, dk, dv, _at(q), _at(k), _at(v), _at(g), per_token,
+                                         _at(state), _at(o), int(flags), _raw_stream(dev))
     if rc != 0:
         raise KdaError(rc, "kda_linattn_decode_step")
     return o
@@ -649,7 +688,7 @@ def kda_linattn_decode_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g
 def _index(t: Optional[torch.Tensor], name: str, dev):
     if t is not None and t.dim() != 1:
         raise ValueError(f"{name} must be a 1-D int32 CUDA tensor")
-    _check(t, name, torch.int32, () if t is None else t.shape, dev)
+    _fits_opt(t, name, torch.int32, () if t is None else t.shape, dev)
 
 
 def _cache(codes, scales, dev):
@@ -657,8 +696,8 @@ def _cache(codes, scales, dev):
         raise ValueError(f"codes has dtype {codes.dtype}, expected int8 or float8_e4m3fn")
     if codes.dim() != 4:
         raise ValueError("codes must be [num_slots,H,d_k,d_v]")
-    _check(codes, "codes", codes.dtype, codes.shape, dev)
-    _check(scales, "scales", torch.float32, codes.shape[:3], dev)
+    _fits_opt(codes, "codes", codes.dtype, codes.shape, dev)
+    _fits_opt(scales, "scales", torch.float32, codes.shape[:3], dev)
     return CACHE_FORMATS[codes.dtype]
 
 
@@ -673,7 +712,7 @@ def kda_state_quantize(states: torch.Tensor, codes: torch.Tensor, scales: torch.
     if states.dim() != 4:
         raise ValueError("states must be [M,H,d_k,d_v]")
     dev = states.device
-    _check(states, "states", torch.float32, states.shape, dev)
+    _fits_opt(states, "states", torch.float32, states.shape, dev)
     fmt = _cache(codes, scales, dev)
     if codes.shape[1:] != states.shape[1:]:
         raise ValueError(f"codes has shape {tuple(codes.shape)}, states {tuple(states.shape)}")
@@ -684,8 +723,8 @@ def kda_state_quantize(states: torch.Tensor, codes: torch.Tensor, scales: torch.
     n = slots.numel() if slots is not None else rows.numel() if rows is not None else states.shape[0]
     M, H, dk, dv = states.shape
     with _launching(stream, dev):
-        rc = lib.kda_state_quantize(fmt, n, M, codes.shape[0], H, dk, dv, _ptr(states), _ptr(rows), _ptr(slots),
-                                    _ptr(codes), _ptr(scales), _stream(stream, dev))
+        rc = lib.kda_state_quantize(fmt, n, M, codes.shape[0], H, dk, dv, _at(states), _at(rows), _at(slots),
+                                    _at(codes), _at(scales), _raw_stream(dev))
     if rc != 0:
         raise KdaError(rc, "kda_state_quantize")
 
@@ -703,9 +742,9 @@ def kda_state_dequantize(codes: torch.Tensor, scales: torch.Tensor, slots: Optio
     with _launching(stream, dev):
         if out is None:
             out = torch.empty((n, H, dk, dv), dtype=torch.float32, device=dev)
-        _check(out, "out", torch.float32, (n, H, dk, dv), dev)
-        rc = lib.kda_state_dequantize(fmt, n, S, H, dk, dv, _ptr(codes), _ptr(scales), _ptr(slots), _ptr(out),
-                                      _stream(stream, dev))
+        _fits_opt(out, "out", torch.float32, (n, H, dk, dv), dev)
+        rc = lib.kda_state_dequantize(fmt, n, S, H, dk, dv, _at(codes), _at(scales), _at(slots), _at(out),
+                                      _raw_stream(dev))
     if rc != 0:
         raise KdaError(rc, "kda_state_dequantize")
     return out

@@ -32,6 +32,10 @@ struct LinRun {
     int num_seqs, T, H;
     const int32_t *cu_seqlens;  // packed batch, or NULL (sequence n is rows n*T .. n*T+T-1)
     long long rows;             // tokens of the whole batch
+    // tensor-core form, token axis in segments: chunks of one (0: not cut), slots of all sequences, and the state
+    // that enters each slot's segment [slot][H][d_x][d_z] with the decay over it [slot][H]
+    int seg_chunks, slots;
+    float *seg_state, *seg_total;
 };
 
 __device__ __forceinline__ int lin_row0(const LinRun &a, int n) { return a.cu_seqlens ? a.cu_seqlens[n] : n * a.T; }
@@ -59,8 +63,16 @@ struct LinGateGrad {
 };
 
 cudaError_t launch_lin_scan(const LinRun &r, int dx, int dz, bool bf16, cudaStream_t st);
+// Chunks of a segment of the tensor-core form, 0 to leave sequences whole; and its slots
+// (segment j of sequence n is slot n + floor(R_n / tokens) + j, R_n its first row).
+int lin_segment_chunks(int num_seqs, int T, int H, long long rows, bool packed);
+inline int lin_segment_slots(int num_seqs, long long rows, int seg_chunks)
+{
+    return (int)(num_seqs + (rows + seg_chunks * 64 - 1) / (seg_chunks * 64));
+}
 // Tensor-core form, bf16 only.
 bool lin_chunk_takes(int dx, int dz);
+cudaError_t launch_lin_states(const LinRun &r, int dx, int dz, cudaStream_t st);       // fills seg_state
 cudaError_t launch_lin_chunk(const LinRun &r, int dx, int dz, cudaStream_t st);        // bf16 outputs
 cudaError_t launch_lin_chunk_fine(const LinRun &r, int dx, int dz, cudaStream_t st);   // fp32 outputs
 // Sums the per-value-head fp32 gradients over the heads that share a key head, casts them, and

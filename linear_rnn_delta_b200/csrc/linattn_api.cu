@@ -91,19 +91,47 @@ bool chunk_form(const LinSizes &s, unsigned flags)
 {
     return s.dtype == KDA_DTYPE_BF16 && !(flags & KDA_FLAG_FORCE_SCAN) && kda::lin_chunk_takes(s.dk, s.dv);
 }
-cudaError_t launch_run(const LinRun &r, int dx, int dz, bool chunk, bool bf16, cudaStream_t st)
+// Segments of the chunk form's token axis: their length and the workspace of their states and decays.
+struct Segments {
+    int chunks, slots;
+    size_t states, totals, total;   // offsets and size in bytes
+};
+Segments segments(const LinSizes &s, bool chunk)
 {
-    return chunk ? (r.out_f32 ? kda::launch_lin_chunk_fine(r, dx, dz, st) : kda::launch_lin_chunk(r, dx, dz, st)) : kda::launch_lin_scan(r, dx, dz, bf16, st);
+    Segments g{};
+    if (chunk) g.chunks = kda::lin_segment_chunks(s.N, s.T, s.H, s.rows, s.packed);
+    if (!g.chunks) return g;
+    g.slots = kda::lin_segment_slots(s.N, s.rows, g.chunks);
+    g.totals = up256((size_t)g.slots * s.H * s.dk * s.dv * 4);
+    g.total = g.totals + up256((size_t)g.slots * s.H * 4);
+    return g;
+}
+// One pass; `seg_ws` holds the segments' workspace.
+cudaError_t launch_run(LinRun r, int dx, int dz, bool chunk, bool bf16, const Segments &g, uint8_t *seg_ws,
+                       cudaStream_t st)
+{
+    if (!chunk) return kda::launch_lin_scan(r, dx, dz, bf16, st);
+    if (g.chunks) {
+        r.seg_chunks = g.chunks;
+        r.slots = g.slots;
+        r.seg_state = reinterpret_cast<float *>(seg_ws + g.states);
+        r.seg_total = reinterpret_cast<float *>(seg_ws + g.totals);
+        const cudaError_t e = kda::launch_lin_states(r, dx, dz, st);
+        if (e != cudaSuccess) return e;
+    }
+    return r.out_f32 ? kda::launch_lin_chunk_fine(r, dx, dz, st) : kda::launch_lin_chunk(r, dx, dz, st);
 }
 
 // Backward workspace regions.
 struct BwdLayout {
-    size_t dqf, dkf, dot_q, dot_k, snap_s, snap_g, partial, total;
+    size_t dqf, dkf, dot_q, dot_k, snap_s, snap_g, partial, seg, total;
     int slots;
+    Segments g;
 };
-BwdLayout bwd_layout(const LinSizes &s)
+BwdLayout bwd_layout(const LinSizes &s, bool chunk)
 {
     BwdLayout L;
+    L.g = segments(s, chunk);
     L.slots = (int)(s.N + (s.rows + kda::LIN_SEG - 1) / kda::LIN_SEG);
     const size_t grad = up256((size_t)s.rows * s.H * s.dk * 4), dots = up256((size_t)s.rows * s.H * 4);
     const size_t snap = up256((size_t)L.slots * s.H * s.dk * s.dv * 4);
@@ -114,7 +142,8 @@ BwdLayout bwd_layout(const LinSizes &s)
     L.snap_s = L.dot_k + dots;
     L.snap_g = L.snap_s + snap;
     L.partial = L.snap_g + snap;
-    L.total = L.partial + up256((size_t)L.slots * s.H * 4);
+    L.seg = L.partial + up256((size_t)L.slots * s.H * 4);
+    L.total = L.seg + L.g.total;
     return L;
 }
 
@@ -125,8 +154,7 @@ extern "C" size_t kda_linattn_chunk_fwd_workspace_size(int dtype, int B, int T, 
 {
     LinSizes s;
     if (lin_sizes(s, dtype, B, T, Hk, H, d_k, d_v, has_cu_seqlens != 0, num_seqs) != KDA_OK) return 0;
-    (void)flags;
-    return 0;
+    return segments(s, chunk_form(s, flags)).total;
 }
 
 extern "C" int kda_linattn_chunk_fwd(int dtype, int B, int T, int Hk, int H, int d_k, int d_v,
@@ -176,7 +204,9 @@ extern "C" int kda_linattn_chunk_fwd(int dtype, int B, int T, int Hk, int H, int
     r.snap = chunk_states;
     r.snap_tokens = kda::SLOT_TOKENS;
     r.out = o;
-    const cudaError_t e = launch_run(r, d_k, d_v, chunk_form(s, flags), dtype == KDA_DTYPE_BF16, st);
+    const bool chunk = chunk_form(s, flags);
+    const cudaError_t e = launch_run(r, d_k, d_v, chunk, dtype == KDA_DTYPE_BF16, segments(s, chunk),
+                                     static_cast<uint8_t *>(workspace), st);
     if (e != cudaSuccess) return cuda_fail(e, "kda_linattn_chunk_fwd launch");
     return KDA_OK;
 }
@@ -186,7 +216,8 @@ extern "C" size_t kda_linattn_chunk_bwd_workspace_size(int dtype, int B, int T, 
 {
     LinSizes s;
     if (lin_sizes(s, dtype, B, T, Hk, H, d_k, d_v, has_cu_seqlens != 0, num_seqs) != KDA_OK) return 0;
-    return bwd_layout(s).total;
+    // the token scan (KDA_FLAG_FORCE_SCAN) needs no more than the chunk form
+    return bwd_layout(s, chunk_form(s, 0u)).total;
 }
 
 extern "C" int kda_linattn_chunk_bwd(int dtype, int B, int T, int Hk, int H, int d_k, int d_v,
@@ -214,13 +245,13 @@ extern "C" int kda_linattn_chunk_bwd(int dtype, int B, int T, int Hk, int H, int
     CHECK(opt_ptr(initial_state, "initial_state"));
     CHECK(opt_ptr(d_final_state, "d_final_state"));
     CHECK(opt_ptr(d_initial_state, "d_initial_state"));
-    const BwdLayout L = bwd_layout(s);
+    const bool chunk = chunk_form(s, flags);
+    const BwdLayout L = bwd_layout(s, chunk);
     if (!workspace || !aligned16(workspace) || workspace_bytes < L.total)
         return fail(KDA_ERR_INVALID_ARG, "kda_linattn_chunk_bwd needs a 16-byte aligned workspace of %zu bytes", L.total);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     const bool bf16 = dtype == KDA_DTYPE_BF16;
-    const bool chunk = chunk_form(s, flags);
     const int group = H / Hk;
     auto f32 = [&](size_t off) { return reinterpret_cast<float *>(ws + off); };
     // dq_t = S_t do_t: forward in time, the state transposed
@@ -233,7 +264,7 @@ extern "C" int kda_linattn_chunk_bwd(int dtype, int B, int T, int Hk, int H, int
     r.snap_tokens = kda::LIN_SEG;
     r.out = f32(L.dqf);
     r.out_f32 = 1;
-    cudaError_t e = launch_run(r, d_v, d_k, chunk, bf16, st);
+    cudaError_t e = launch_run(r, d_v, d_k, chunk, bf16, L.g, ws + L.seg, st);
     if (e != cudaSuccess) return cuda_fail(e, "kda_linattn_chunk_bwd dq");
     // dk_t = G_t v_t: backward in time, the state transposed
     r = base_run(s, g, g_per_token, cu_seqlens);
@@ -246,7 +277,7 @@ extern "C" int kda_linattn_chunk_bwd(int dtype, int B, int T, int Hk, int H, int
     r.snap_tokens = kda::LIN_SEG;
     r.out = f32(L.dkf);
     r.out_f32 = 1;
-    if ((e = launch_run(r, d_v, d_k, chunk, bf16, st)) != cudaSuccess) return cuda_fail(e, "kda_linattn_chunk_bwd dk");
+    if ((e = launch_run(r, d_v, d_k, chunk, bf16, L.g, ws + L.seg, st)) != cudaSuccess) return cuda_fail(e, "kda_linattn_chunk_bwd dk");
     // dv_t = G_t^T k_t: backward in time
     r = base_run(s, g, g_per_token, cu_seqlens);
     r.reverse = 1;
@@ -255,7 +286,7 @@ extern "C" int kda_linattn_chunk_bwd(int dtype, int B, int T, int Hk, int H, int
     r.s_in = d_final_state;
     r.s_out = d_initial_state;
     r.out = dv;
-    if ((e = launch_run(r, d_k, d_v, chunk, bf16, st)) != cudaSuccess) return cuda_fail(e, "kda_linattn_chunk_bwd dv");
+    if ((e = launch_run(r, d_k, d_v, chunk, bf16, L.g, ws + L.seg, st)) != cudaSuccess) return cuda_fail(e, "kda_linattn_chunk_bwd dv");
     if ((e = kda::launch_lin_share(f32(L.dqf), f32(L.dkf), q, k, dq, dk, f32(L.dot_q), f32(L.dot_k), s.rows, Hk, H,
                                    d_k, bf16, st)) != cudaSuccess)
         return cuda_fail(e, "kda_linattn_chunk_bwd head sums");

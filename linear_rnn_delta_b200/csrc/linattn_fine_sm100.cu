@@ -68,11 +68,13 @@ __global__ void __launch_bounds__(NT, 1) lin_chunk_fine_kernel(const __grid_cons
     GateStage *gates = reinterpret_cast<GateStage *>(sm + SM_GATE);
     const LinRun &a = P.a;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, wg = warp >> 2;
-    const int n = blockIdx.x / a.H, h = blockIdx.x % a.H;
-    const int row0 = lin_row0(a, n), len = lin_len(a, n);
-    const int nch = (len + C - 1) / C;
+    const int h = blockIdx.x % a.H;
     const bool rev = a.reverse != 0;
-    const size_t soff = ((size_t)n * a.H + h) * DX * DZ;
+    const Work work = lin_work(a, blockIdx.x / a.H);
+    const int n = work.n, row0 = work.row0, len = work.len, nch = work.nch;
+    if (a.seg_chunks && nch <= 0) return;
+    const bool closing = rev ? work.c0 == 0 : work.c0 + nch == work.nall;   // the sequence's last segment in time
+    const size_t soff = ((size_t)n * a.H + h) * DX * DZ, woff = ((size_t)work.slot * a.H + h) * DX * DZ;
 
     if (warp == 3) tmem_alloc(s_tmem, TM_COLS);
     if (tid == 0) {
@@ -103,7 +105,7 @@ __global__ void __launch_bounds__(NT, 1) lin_chunk_fine_kernel(const __grid_cons
     const uint32_t tbase = *s_tmem;
     const uint32_t tlane = tbase + ((uint32_t)((warp & 3) * 32) << 16);
     // chunk of iteration i
-    auto chunk = [&](int i) { return rev ? nch - 1 - i : i; };
+    auto chunk = [&](int i) { return work.c0 + (rev ? nch - 1 - i : i); };
     // phase parity of the i-th use of a barrier that alternates between NB
     auto par = [](int i) { return (uint32_t)(i / NB) & 1u; };
 
@@ -560,12 +562,14 @@ __global__ void __launch_bounds__(NT, 1) lin_chunk_fine_kernel(const __grid_cons
         if ((warp & 3) < JW) {
             const int j = (warp & 3) * 32 + lane, i0 = (wg - 4) * CX;
             float2 S[CX / 2];
-            if (a.s_in && a.in_t) {
+            const float *s_in = a.seg_chunks ? a.seg_state + woff : a.s_in ? a.s_in + soff : nullptr;
+            float *s_out = a.s_out && closing ? a.s_out + soff : nullptr;
+            if (s_in && a.in_t && !a.seg_chunks) {
 #pragma unroll
                 for (int e = 0; e < CX / 2; ++e)
-                    S[e] = *reinterpret_cast<const float2 *>(a.s_in + soff + (size_t)j * DX + i0 + 2 * e);
-            } else if (a.s_in) {
-                const float *at = a.s_in + soff + (size_t)i0 * DZ + j;
+                    S[e] = *reinterpret_cast<const float2 *>(s_in + (size_t)j * DX + i0 + 2 * e);
+            } else if (s_in) {
+                const float *at = s_in + (size_t)i0 * DZ + j;
 #pragma unroll
                 for (int e = 0; e < CX / 2; ++e) S[e] = make_float2(at[2 * e * DZ], at[(2 * e + 1) * DZ]);
             } else {
@@ -577,10 +581,11 @@ __global__ void __launch_bounds__(NT, 1) lin_chunk_fine_kernel(const __grid_cons
             for (int i = 0;; ++i) {
                 float *to[2] = {nullptr, nullptr};
                 // the token whose boundary this state is: backward the chunk to come ends there, forward the last one did
-                const int edge = rev ? (i < nch ? min(len, (chunk(i) + 1) * C) - 1 : -1) : min(len, i * C) - 1;
+                const int edge = rev ? (i < nch ? min(len, (chunk(i) + 1) * C) - 1 : -1)
+                                     : (i > 0 ? min(len, (work.c0 + i) * C) - 1 : -1);
                 if (a.snap && edge >= 0 && (edge == len - 1 || (edge + 1) % a.snap_tokens == 0))
                     to[0] = a.snap + ((size_t)(n + row0 / a.snap_tokens + edge / a.snap_tokens) * a.H + h) * DX * DZ;
-                if (i == nch && a.s_out) to[1] = a.s_out + soff;
+                if (i == nch) to[1] = s_out;
 #pragma unroll 1
                 for (int w = 0; w < 2; ++w) {
                     float *dst = w ? to[1] : to[0];
@@ -638,8 +643,8 @@ __global__ void __launch_bounds__(NT, 1) lin_chunk_fine_kernel(const __grid_cons
                 }
                 warp_arrive(bar + B_EMPTY + s);
             }
-            if (!ok && a.s_out)
-                for (int e = 0; e < CX; ++e) a.s_out[soff + (size_t)(i0 + e) * DZ + j] = __int_as_float(0x7fc00000);
+            if (!ok && s_out)
+                for (int e = 0; e < CX; ++e) s_out[(size_t)(i0 + e) * DZ + j] = __int_as_float(0x7fc00000);
         }
     }
     tc_fence_before();
@@ -663,7 +668,7 @@ template <int DX, int DZ, int NSP, int NPP, typename TOut> cudaError_t launch_di
                      !make_map(&p.tz, r.z, rows, r.H / r.gz, DZ) ||
                      (sizeof(TOut) == 2 && !make_map(&p.to, r.out, rows, r.H, DZ))))
         return cudaErrorInvalidValue;
-    lin_chunk_fine_kernel<DX, DZ, NSP, NPP, TOut><<<(unsigned)(r.num_seqs * r.H), NT, SM_ALLOC, st>>>(p);
+    lin_chunk_fine_kernel<DX, DZ, NSP, NPP, TOut><<<(unsigned)((r.seg_chunks ? r.slots : r.num_seqs) * r.H), NT, SM_ALLOC, st>>>(p);
     return cudaGetLastError();
 }
 

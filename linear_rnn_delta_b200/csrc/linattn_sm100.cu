@@ -40,6 +40,9 @@
 // carry a token's z to tokens it must not reach.  Warps 4-11 look for them; in a chunk that has any they
 // are taken out of Z, and the outputs of that channel from that token on, and the channel's state, become
 // NaN instead.
+#include <algorithm>
+#include <cmath>
+
 #include "linattn_sm100.cuh"
 
 namespace kda {
@@ -84,7 +87,8 @@ struct LinChunkParams {
     unsigned *status;
 };
 
-template <int DX, int DZ>
+// STATE: only the state that a segment adds from nothing, and its decay.
+template <int DX, int DZ, bool STATE>
 __global__ void __launch_bounds__(NT, 1) lin_chunk_kernel(const __grid_constant__ LinChunkParams P)
 {
     constexpr int JW = DZ / 32;                // warps with value channels of their own
@@ -97,11 +101,14 @@ __global__ void __launch_bounds__(NT, 1) lin_chunk_kernel(const __grid_constant_
     GateStage *gates = reinterpret_cast<GateStage *>(sm + SM_GATE);
     const LinRun &a = P.a;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, wg = warp >> 2;
-    const int n = blockIdx.x / a.H, h = blockIdx.x % a.H;
-    const int row0 = lin_row0(a, n), len = lin_len(a, n);
-    const int nch = (len + C - 1) / C;
+    const int h = blockIdx.x % a.H;
     const bool rev = a.reverse != 0;
-    const size_t soff = ((size_t)n * a.H + h) * DX * DZ;
+    const Work work = lin_work(a, blockIdx.x / a.H);
+    const int n = work.n, row0 = work.row0, len = work.len, nch = work.nch;
+    if (a.seg_chunks && nch <= 0) return;
+    const bool closing = rev ? work.c0 == 0 : work.c0 + nch == work.nall;   // the sequence's last segment in time
+    if (STATE && closing) return;   // nobody asks for the state behind it
+    const size_t soff = ((size_t)n * a.H + h) * DX * DZ, woff = ((size_t)work.slot * a.H + h) * DX * DZ;
 
     if (warp == 3) tmem_alloc(s_tmem, TM_COLS);
     if (tid == 0) {
@@ -109,7 +116,7 @@ __global__ void __launch_bounds__(NT, 1) lin_chunk_kernel(const __grid_constant_
         for (int s = 0; s < NS; ++s) {
             mbar_init(bar + B_FULL + s, 1);
             mbar_init(bar + B_GATE + s, 1);
-            mbar_init(bar + B_EMPTY + s, 1 + 2 * JW + 4);   // products, state, outputs
+            mbar_init(bar + B_EMPTY + s, 1 + 2 * JW + (STATE ? 0 : 4));   // products, state, outputs
         }
         mbar_init(bar + B_QKF, 1);
         mbar_init(bar + B_QKE, 2);
@@ -133,11 +140,12 @@ __global__ void __launch_bounds__(NT, 1) lin_chunk_kernel(const __grid_constant_
     const uint32_t tbase = *s_tmem;
     const uint32_t tlane = tbase + ((uint32_t)((warp & 3) * 32) << 16);
     // chunk of iteration i
-    auto chunk = [&](int i) { return rev ? nch - 1 - i : i; };
+    auto chunk = [&](int i) { return work.c0 + (rev ? nch - 1 - i : i); };
 
     if (wg == 0) {
         regs_dec<RG_P>();
         if (warp < 2) {
+          if constexpr (!STATE) {
             // ---- P: row r of QK
             const int r = tid;
             for (int i = 0; i < nch; ++i) {
@@ -199,6 +207,7 @@ __global__ void __launch_bounds__(NT, 1) lin_chunk_kernel(const __grid_constant_
                 fence_async_smem();
                 warp_arrive(bar + B_PF + pb);
             }
+          }
         } else if (warp == 2) {
             // ---- loads and decays (a chunk's log-decays are on their way while the one before is summed)
             float next[2] = {0.f, 0.f};
@@ -211,16 +220,18 @@ __global__ void __launch_bounds__(NT, 1) lin_chunk_kernel(const __grid_constant_
                 }
             };
             if (nch > 0) gate_load(0);
+            long long sum = 0;   // of the segment's log-decays
+            bool any_nan = false;
             int i = 0;
             for (; i < nch; ++i) {
                 const int s = i % NS, t0 = chunk(i) * C;
                 if (i >= NS && !wait(bar + B_EMPTY + s, (i / NS - 1) & 1, s_abort)) break;
                 if (lane == 0) {
                     uint8_t *st = sm + s * STAGE;
-                    mbar_expect_tx(bar + B_FULL + s, (2 * DX + DZ) * C * 2);
+                    mbar_expect_tx(bar + B_FULL + s, ((STATE ? 1 : 2) * DX + DZ) * C * 2);
 #pragma unroll
                     for (int p = 0; p < DX / 64; ++p) {
-                        tma_load_3d(st + p * 8192, &P.tx, bar + B_FULL + s, p * 64, h / a.gx, row0 + t0);
+                        if (!STATE) tma_load_3d(st + p * 8192, &P.tx, bar + B_FULL + s, p * 64, h / a.gx, row0 + t0);
                         tma_load_3d(st + TILE + p * 8192, &P.ty, bar + B_FULL + s, p * 64, h / a.gy, row0 + t0);
                     }
 #pragma unroll
@@ -262,6 +273,7 @@ __global__ void __launch_bounds__(NT, 1) lin_chunk_kernel(const __grid_constant_
                     G.w[t] = w;
                     G.u[t] = u;
                 }
+                if (STATE) sum += end, any_nan = any_nan || (nan_a | nan_b);
                 narrow = __all_sync(0xffffffffu, narrow);
                 if (lane == 0) {
                     G.total = (nan_a | nan_b) ? nan : fix_exp2(end);
@@ -270,6 +282,8 @@ __global__ void __launch_bounds__(NT, 1) lin_chunk_kernel(const __grid_constant_
                 }
                 warp_arrive(bar + B_GATE + s);
             }
+            if (STATE && lane == 0)
+                a.seg_total[(size_t)work.slot * a.H + h] = any_nan ? __int_as_float(0x7fc00000) : fix_exp2(sum);
             // no load is in flight when the CTA ends, wound down early or not
             if (lane == 0)
                 for (int j = max(0, i - NS); j < i; ++j) mbar_wait_cycles(bar + B_FULL + j % NS, (j / NS) & 1, WAIT_LIMIT);
@@ -293,8 +307,9 @@ __global__ void __launch_bounds__(NT, 1) lin_chunk_kernel(const __grid_constant_
                         for (int kk = 0; kk < C / 16; ++kk)
                             mma_bf16_ts_warp(tbase + TM_KV, tbase + TM_ZP + p * 32 + kk * 8, dMN(y, kk), ID_KV, p + kk > 0, lead);
                     mma_commit_warp(bar + B_KVF, lead);
+                    if (STATE) mma_commit_warp(bar + B_EMPTY + i % NS, lead);
                 }
-                if (i + 1 < nch) {   // QK of the next one; rows 64-127 of A are what lies behind X: lanes nobody reads
+                if (!STATE && i + 1 < nch) {   // QK of the next one; rows 64-127 of A are what lies behind X: lanes nobody reads
                     const int sn = (i + 1) % NS;
                     const uint32_t x = k_tile(sb + sn * STAGE), y = k_tile(sb + sn * STAGE + TILE);
                     ok = wait(bar + B_FULL + sn, ((i + 1) / NS) & 1, s_abort) &&
@@ -308,7 +323,7 @@ __global__ void __launch_bounds__(NT, 1) lin_chunk_kernel(const __grid_constant_
                             mma_bf16_warp(tbase + TM_QK, dK(x, kk) + p * 512, dK(y, kk) + p * 512, ID_QK, p + kk > 0, lead);
                     mma_commit_warp(bar + B_QKF, lead);
                 }
-                if (i < 0) continue;
+                if (STATE || i < 0) continue;
                 ok = wait(bar + B_SF, i & 1, s_abort) && (i == 0 || wait(bar + B_OE, (i - 1) & 1, s_abort));
                 if (!ok) break;
                 tc_fence_after();
@@ -404,7 +419,7 @@ __global__ void __launch_bounds__(NT, 1) lin_chunk_kernel(const __grid_constant_
                 group_sync(1, ZT);   // once more, without them
             }
             if (i > 0) ok = wait(bar + B_KVF, (i - 1) & 1, s_abort);   // KV_{i-1} has read the parts
-            if (!G.narrow) {   // w_r goes to X, which QK_i has read
+            if (!STATE && !G.narrow) {   // w_r goes to X, which QK_i has read
                 ok = ok && wait(bar + B_QKF, i & 1, s_abort);
 #pragma unroll 1
                 for (int e = t; e < C * DX / 8; e += ZT) {
@@ -443,6 +458,7 @@ __global__ void __launch_bounds__(NT, 1) lin_chunk_kernel(const __grid_constant_
                 tc_fence_before();
             }
             warp_arrive(bar + B_KBF);
+            if (STATE) continue;
             // Z^T itself: O_{i-1} has read the last one
             if (i > 0) ok = ok && wait(bar + B_OF + ((i - 1) & 1), ((i - 1) >> 1) & 1, s_abort);
             if (!ok) continue;
@@ -457,6 +473,7 @@ __global__ void __launch_bounds__(NT, 1) lin_chunk_kernel(const __grid_constant_
         }
     } else if (wg == 3) {
         regs_dec<RG_OUT>();
+      if constexpr (!STATE) {
         // ---- outputs: fragments of O^T (channel, token pair) go transposed into [token][channel] panels over
         // this stage's X, which nobody reads any more, and leave from there by TMA (the last, ragged chunk of
         // a sequence row by row: what lies behind it is another sequence's)
@@ -532,6 +549,7 @@ __global__ void __launch_bounds__(NT, 1) lin_chunk_kernel(const __grid_constant_
             warp_arrive(bar + B_EMPTY + s);
         }
         bulk_wait_all();
+      }
     } else {
         regs_inc<RG_STATE>();
         // ---- state: row j of R^T, half of its columns
@@ -539,12 +557,14 @@ __global__ void __launch_bounds__(NT, 1) lin_chunk_kernel(const __grid_constant_
         if ((warp & 3) < JW) {
             const int j = (warp & 3) * 32 + lane, i0 = (wg - 4) * CX;
             float2 S[CX / 2];
-            if (a.s_in && a.in_t) {
+            const float *s_in = STATE ? nullptr : a.seg_chunks ? a.seg_state + woff : a.s_in ? a.s_in + soff : nullptr;
+            float *s_out = STATE ? a.seg_state + woff : a.s_out && closing ? a.s_out + soff : nullptr;
+            if (s_in && a.in_t && !a.seg_chunks) {
 #pragma unroll
                 for (int e = 0; e < CX / 2; ++e)
-                    S[e] = *reinterpret_cast<const float2 *>(a.s_in + soff + (size_t)j * DX + i0 + 2 * e);
-            } else if (a.s_in) {
-                const float *at = a.s_in + soff + (size_t)i0 * DZ + j;
+                    S[e] = *reinterpret_cast<const float2 *>(s_in + (size_t)j * DX + i0 + 2 * e);
+            } else if (s_in) {
+                const float *at = s_in + (size_t)i0 * DZ + j;
 #pragma unroll
                 for (int e = 0; e < CX / 2; ++e) S[e] = make_float2(at[2 * e * DZ], at[(2 * e + 1) * DZ]);
             } else {
@@ -554,14 +574,15 @@ __global__ void __launch_bounds__(NT, 1) lin_chunk_kernel(const __grid_constant_
             bool ok = true;
             // iteration i: the state before it is published (and written where it is a boundary's or the last)
             for (int i = 0;; ++i) {
-                if (a.snap || i == nch) {
+                if ((!STATE && a.snap) || i == nch) {
                     float *to[2] = {nullptr, nullptr};
                     // the token whose boundary this state is: backward the chunk to come ends there, forward the
                     // last one did
-                    const int edge = rev ? (i < nch ? min(len, (chunk(i) + 1) * C) - 1 : -1) : min(len, i * C) - 1;
-                    if (a.snap && edge >= 0 && (edge == len - 1 || (edge + 1) % a.snap_tokens == 0))
+                    const int edge = rev ? (i < nch ? min(len, (chunk(i) + 1) * C) - 1 : -1)
+                                         : (i > 0 ? min(len, (work.c0 + i) * C) - 1 : -1);
+                    if (!STATE && a.snap && edge >= 0 && (edge == len - 1 || (edge + 1) % a.snap_tokens == 0))
                         to[0] = a.snap + ((size_t)(n + row0 / a.snap_tokens + edge / a.snap_tokens) * a.H + h) * DX * DZ;
-                    if (i == nch && a.s_out) to[1] = a.s_out + soff;
+                    if (i == nch) to[1] = s_out;
 #pragma unroll 1
                     for (int w = 0; w < 2; ++w) {
                         float *dst = w ? to[1] : to[0];
@@ -575,6 +596,7 @@ __global__ void __launch_bounds__(NT, 1) lin_chunk_kernel(const __grid_constant_
                     }
                     if (i == nch) break;
                 }
+              if constexpr (!STATE) {
                 if (i > 0) {
                     ok = wait(bar + B_SE, (i - 1) & 1, s_abort);   // O_{i-1} has read the parts
                     if (!ok) break;
@@ -595,6 +617,7 @@ __global__ void __launch_bounds__(NT, 1) lin_chunk_kernel(const __grid_constant_
                 tmem_wait_st();
                 tc_fence_before();
                 warp_arrive(bar + B_SF);
+              }
                 const int s = i % NS;
                 ok = wait(bar + B_KVF, i & 1, s_abort);
                 if (!ok) break;
@@ -618,8 +641,8 @@ __global__ void __launch_bounds__(NT, 1) lin_chunk_kernel(const __grid_constant_
                 }
                 warp_arrive(bar + B_EMPTY + s);
             }
-            if (!ok && a.s_out)
-                for (int e = 0; e < CX; ++e) a.s_out[soff + (size_t)(i0 + e) * DZ + j] = __int_as_float(0x7fc00000);
+            if (!ok && s_out)
+                for (int e = 0; e < CX; ++e) s_out[(size_t)(i0 + e) * DZ + j] = __int_as_float(0x7fc00000);
         }
     }
     tc_fence_before();
@@ -629,25 +652,114 @@ __global__ void __launch_bounds__(NT, 1) lin_chunk_kernel(const __grid_constant_
     if (tid == 0 && *s_abort) atomicOr(P.status, DEV_WAIT_TIMEOUT);
 }
 
+// The states that enter the segments, in place of what each adds: one pass over a sequence's segments in time.
+// A thread has 4 values of one (sequence, head)'s state.
+__global__ void __launch_bounds__(256) lin_segment_kernel(const LinRun a, int dx, int dz)
+{
+    const int nh = blockIdx.x, n = nh / a.H, h = nh % a.H, size = dx * dz;
+    const int e = (blockIdx.y * 256 + threadIdx.x) * 4;
+    if (e >= size) return;
+    const int row0 = lin_row0(a, n), len = lin_len(a, n), tokens = a.seg_chunks * C;
+    const int first = n + row0 / tokens, nseg = (len + tokens - 1) / tokens;
+    float4 cur = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (a.s_in) {
+        const float *s = a.s_in + (size_t)nh * size;
+        if (a.in_t) {   // stored [dz][dx]; 4 values of a row i are 4 rows there
+            const int i = e / dz, j = e % dz;
+            cur = make_float4(s[j * dx + i], s[(j + 1) * dx + i], s[(j + 2) * dx + i], s[(j + 3) * dx + i]);
+        } else {
+            cur = *reinterpret_cast<const float4 *>(s + e);
+        }
+    }
+    for (int t = 0; t < nseg; ++t) {
+        const size_t slot = (size_t)(first + (a.reverse ? nseg - 1 - t : t)) * a.H + h;
+        float4 *at = reinterpret_cast<float4 *>(a.seg_state + slot * size + e);
+        const float4 add = t + 1 < nseg ? *at : cur;
+        *at = cur;
+        if (t + 1 < nseg) {
+            const float d = a.seg_total[slot];
+            cur = make_float4(fmaf(d, cur.x, add.x), fmaf(d, cur.y, add.y), fmaf(d, cur.z, add.z), fmaf(d, cur.w, add.w));
+        }
+    }
+    if (nseg == 0 && a.s_out) *reinterpret_cast<float4 *>(a.s_out + (size_t)nh * size + e) = cur;
+}
+
+template <int DX, int DZ> cudaError_t make_params(LinChunkParams &p, const LinRun &r)
+{
+    memset(&p, 0, sizeof(p));
+    p.a = r;
+    const cudaError_t e = device_status_word(&p.status);
+    if (e != cudaSuccess) return e;
+    if (r.rows > 0 && (!make_map(&p.tx, r.x, r.rows, r.H / r.gx, DX) || !make_map(&p.ty, r.y, r.rows, r.H / r.gy, DX) ||
+                       !make_map(&p.tz, r.z, r.rows, r.H / r.gz, DZ) ||
+                       (!r.out_f32 && !make_map(&p.to, r.out, r.rows, r.H, DZ))))
+        return cudaErrorInvalidValue;
+    return cudaSuccess;
+}
+
 template <int DX, int DZ> cudaError_t launch_dims(const LinRun &r, cudaStream_t st)
 {
     static bool done[64] = {};
-    cudaError_t e = opt_in(lin_chunk_kernel<DX, DZ>, SM_ALLOC, done);
+    cudaError_t e = opt_in(lin_chunk_kernel<DX, DZ, false>, SM_ALLOC, done);
     if (e != cudaSuccess) return e;
     LinChunkParams p;
-    memset(&p, 0, sizeof(p));
-    p.a = r;
-    if ((e = device_status_word(&p.status)) != cudaSuccess) return e;
-    if (r.rows > 0 && (!make_map(&p.tx, r.x, r.rows, r.H / r.gx, DX) || !make_map(&p.ty, r.y, r.rows, r.H / r.gy, DX) ||
-                       !make_map(&p.tz, r.z, r.rows, r.H / r.gz, DZ) || !make_map(&p.to, r.out, r.rows, r.H, DZ)))
-        return cudaErrorInvalidValue;
-    lin_chunk_kernel<DX, DZ><<<(unsigned)(r.num_seqs * r.H), NT, SM_ALLOC, st>>>(p);
+    if ((e = make_params<DX, DZ>(p, r)) != cudaSuccess) return e;
+    const unsigned units = (unsigned)(r.seg_chunks ? r.slots : r.num_seqs);
+    lin_chunk_kernel<DX, DZ, false><<<units * r.H, NT, SM_ALLOC, st>>>(p);
+    return cudaGetLastError();
+}
+
+template <int DX, int DZ> cudaError_t launch_states_dims(const LinRun &r, cudaStream_t st)
+{
+    static bool done[64] = {};
+    cudaError_t e = opt_in(lin_chunk_kernel<DX, DZ, true>, SM_ALLOC, done);
+    if (e != cudaSuccess) return e;
+    LinChunkParams p;
+    if ((e = make_params<DX, DZ>(p, r)) != cudaSuccess) return e;
+    lin_chunk_kernel<DX, DZ, true><<<(unsigned)(r.slots * r.H), NT, SM_ALLOC, st>>>(p);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    lin_segment_kernel<<<dim3(r.num_seqs * r.H, (DX * DZ + 1023) / 1024), 256, 0, st>>>(r, DX, DZ);
     return cudaGetLastError();
 }
 
 }  // namespace
 
 bool lin_chunk_takes(int dx, int dz) { return (dx == 64 || dx == 128) && (dz == 64 || dz == 128); }
+
+int lin_segment_chunks(int num_seqs, int T, int H, long long rows, bool packed)
+{
+    // Time in chunks of the kernel's walk.  Whole sequences: the waves of (sequence, head) pairs over the SMs, or
+    // (packed, lengths unknown here) a longest sequence of three times the mean.  Cut: every chunk is walked twice, the
+    // first time for its state alone (half a chunk's time), and a segment's start costs about 4 chunks.
+    const int S = 148;
+    const double units = (double)num_seqs * H, all = (double)((rows + C - 1) / C) * H;
+    const double mean = packed ? all / units : (double)((T + C - 1) / C);
+    double whole = std::ceil(units / S) * mean;
+    if (packed) whole = std::max(whole, std::min(all / H, 3 * mean));
+    int best = 0;
+    for (int waves = 1; waves <= 4; ++waves) {
+        // packed: a sequence's last segment is half empty on average
+        const int seg = std::max(4, packed ? (int)std::ceil(all / (waves * (double)S))
+                                           : (int)std::ceil(mean / std::max(1.0, std::floor(waves * (double)S / units))));
+        if (seg >= mean * (packed ? 3 : 1)) continue;
+        const double count = packed ? units * 0.5 + all / seg : units * std::ceil(mean / seg);
+        const double cut = std::ceil(count / S) * (1.5 * seg + 4) + 4;
+        if (cut < 0.9 * whole) {
+            whole = cut / 0.9;
+            best = seg;
+        }
+    }
+    return best;
+}
+
+cudaError_t launch_lin_states(const LinRun &r, int dx, int dz, cudaStream_t st)
+{
+    if (dx == 128 && dz == 128) return launch_states_dims<128, 128>(r, st);
+    if (dx == 128 && dz == 64) return launch_states_dims<128, 64>(r, st);
+    if (dx == 64 && dz == 128) return launch_states_dims<64, 128>(r, st);
+    if (dx == 64 && dz == 64) return launch_states_dims<64, 64>(r, st);
+    return cudaErrorInvalidValue;
+}
 
 cudaError_t launch_lin_chunk(const LinRun &r, int dx, int dz, cudaStream_t st)
 {

@@ -22,6 +22,33 @@ constexpr long long WAIT_LIMIT = 1ll << 32;           // cycles, about 2 s (the 
 constexpr uint32_t WAIT_NS = 1000000, WAIT_POLLS = 2000;   // a poll sleeps for up to 1 ms: about 2 s
 constexpr unsigned DEV_WAIT_TIMEOUT = 1u;
 
+// What a CTA walks: chunks c0 .. c0 + nch - 1 of sequence n (nall in all; none: the slot is nobody's).
+struct Work {
+    int n, slot, row0, len, c0, nch, nall;
+};
+__device__ __forceinline__ Work lin_work(const LinRun &a, int unit)
+{
+    Work w;
+    w.slot = unit;
+    if (a.seg_chunks) {   // the last sequence whose first slot is not behind this one (first slots increase)
+        int lo = 0, hi = a.num_seqs - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) / 2;
+            if (mid + lin_row0(a, mid) / (a.seg_chunks * C) <= unit) lo = mid;
+            else hi = mid - 1;
+        }
+        w.n = lo;
+    } else {
+        w.n = unit;
+    }
+    w.row0 = lin_row0(a, w.n);
+    w.len = lin_len(a, w.n);
+    w.nall = (w.len + C - 1) / C;
+    w.c0 = a.seg_chunks ? (unit - w.n - w.row0 / (a.seg_chunks * C)) * a.seg_chunks : 0;
+    w.nch = a.seg_chunks ? min(a.seg_chunks, w.nall - w.c0) : w.nall;
+    return w;
+}
+
 // Descriptors (low words): K step kk of a K-major tile in panels of 64 elements, and of an MN-major
 // [token][channel] tile in panels of 64 channels; `base` the tile's own.
 __device__ __forceinline__ uint32_t k_tile(uint32_t saddr) { return desc_sw128_lo(saddr, 16); }
