@@ -12,6 +12,7 @@ fails if the library has not been built.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional, Union
 
@@ -555,6 +556,16 @@ def _launching(stream, dev):
     return torch.cuda.stream(stream)
 
 
+@functools.lru_cache(maxsize=256)
+def _lin_fwd_workspace(*sizes):
+    return lib.kda_linattn_chunk_fwd_workspace_size(*sizes)
+
+
+@functools.lru_cache(maxsize=256)
+def _lin_bwd_workspace(*sizes):
+    return lib.kda_linattn_chunk_bwd_workspace_size(*sizes)
+
+
 def _raw_stream(dev):
     """The current stream of the (current) device, which _launching has made the launching one."""
     return torch._C._cuda_getCurrentRawStream(dev.index)
@@ -579,26 +590,28 @@ def kda_linattn_chunk_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: 
     dt, dev, Hk, H, dk, dv, per_token = _lin_inputs(q, k, v, g, True)
     B, T = q.shape[:2]
     N = _num_seqs(cu_seqlens, B, dev)
-    f32 = dict(dtype=torch.float32, device=dev)
     states, snaps = (N, H, dk, dv), (num_chunk_slots(B, T, N), H, dk, dv)
     want_states = chunk_states is not None and chunk_states is not False
     _fits_opt(initial_state, "initial_state", torch.float32, states, dev)
     sizes = (_DTYPES[dt], B, T, Hk, H, dk, dv)
     with _launching(stream, dev):
         if final_state is True:
-            final_state = torch.empty(states, **f32)
+            final_state = g.new_empty(states)
         elif final_state is False:
             final_state = None
+        else:
+            _fits_opt(final_state, "final_state", torch.float32, states, dev)
         if chunk_states is True:
-            chunk_states = torch.empty(snaps, **f32)
+            chunk_states = g.new_empty(snaps)
         elif chunk_states is False:
             chunk_states = None
+        else:
+            _fits_opt(chunk_states, "chunk_states", torch.float32, snaps, dev)
         if o is None:
-            o = torch.empty((B, T, H, dv), dtype=dt, device=dev)
-        _fits_opt(final_state, "final_state", torch.float32, states, dev)
-        _fits_opt(o, "o", dt, (B, T, H, dv), dev)
-        _fits_opt(chunk_states, "chunk_states", torch.float32, snaps, dev)
-        ws_bytes = lib.kda_linattn_chunk_fwd_workspace_size(*sizes, int(cu_seqlens is not None), N, int(flags))
+            o = torch.empty_like(v)
+        else:
+            _fits(o, "o", dt, v.shape, dev)
+        ws_bytes = _lin_fwd_workspace(*sizes, int(cu_seqlens is not None), N, int(flags))
         ws = torch.empty(ws_bytes, dtype=torch.uint8, device=dev) if ws_bytes else None
         rc = lib.kda_linattn_chunk_fwd(*sizes, _at(q), _at(k), _at(v), _at(g), per_token, _at(cu_seqlens), N,
                                        _at(initial_state), _at(final_state), _at(chunk_states), _at(o), _at(ws),
@@ -629,8 +642,8 @@ def kda_linattn_chunk_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: 
     sizes = (_DTYPES[dt], B, T, Hk, H, dk, dv)
     with _launching(stream, dev):
         dqt, dkt, dvt, dgt = (torch.empty_like(x) for x in (q, k, v, g))
-        ds0 = torch.empty((N, H, dk, dv), dtype=torch.float32, device=dev) if d_initial_state else None
-        ws_bytes = lib.kda_linattn_chunk_bwd_workspace_size(*sizes, int(cu_seqlens is not None), N)
+        ds0 = g.new_empty((N, H, dk, dv)) if d_initial_state else None
+        ws_bytes = _lin_bwd_workspace(*sizes, int(cu_seqlens is not None), N)
         if ws_bytes == 0:
             raise KdaError(1, "kda_linattn_chunk_bwd_workspace_size")
         ws = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
@@ -676,8 +689,9 @@ def kda_linattn_decode_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g
     _fits_opt(state, "state", torch.float32, (N, H, dk, dv), dev)
     with _launching(stream, dev):
         if o is None:
-            o = torch.empty((N, H, dv), dtype=dt, device=dev)
-        _fits_opt(o, "o", dt, (N, H, dv), dev)
+            o = torch.empty_like(v)
+        else:
+            _fits(o, "o", dt, v.shape, dev)
         rc = lib.kda_linattn_decode_step(_DTYPES[dt], N, Hk, H, dk, dv, _at(q), _at(k), _at(v), _at(g), per_token,
                                          _at(state), _at(o), int(flags), _raw_stream(dev))
     if rc != 0:
@@ -741,8 +755,9 @@ def kda_state_dequantize(codes: torch.Tensor, scales: torch.Tensor, slots: Optio
     n = S if slots is None else slots.numel()
     with _launching(stream, dev):
         if out is None:
-            out = torch.empty((n, H, dk, dv), dtype=torch.float32, device=dev)
-        _fits_opt(out, "out", torch.float32, (n, H, dk, dv), dev)
+            out = scales.new_empty((n, H, dk, dv))
+        else:
+            _fits(out, "out", torch.float32, (n, H, dk, dv), dev)
         rc = lib.kda_state_dequantize(fmt, n, S, H, dk, dv, _at(codes), _at(scales), _at(slots), _at(out),
                                       _raw_stream(dev))
     if rc != 0:

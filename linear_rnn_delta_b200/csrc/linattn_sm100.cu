@@ -26,14 +26,15 @@
 // point, so that a strong decay costs the pairs on one side of it nothing; those below -10^4 count as
 // -10^4, whose e^g is 0, so that -infinity needs no case of its own.
 //
-// A CTA of 24 warps walks one (sequence, head), with a bounded wait on every mbarrier:
+// A CTA of 28 warps walks one (sequence, head), or a segment of one, with a bounded wait on every mbarrier:
 //   warps 0-1   P: QK lanes 0-63 (a thread has row r) -> decay, mask -> shared memory, two buffers
-//   warp 2      loads (TMA, four stages of X, Y, Z) and the chunk's decays
-//   warp 3      issues every MMA, in the order KV_i, QK_{i+1}, O_i: the state's way from KV_i to O_{i+1} has
-//               the other products in between
+//   warp 2      the chunk's decays
 //   warps 4-11  Z^T and its scaled parts to tensor memory
 //   warps 12-15 outputs: w_r O -> bf16 -> [token][channel] tile -> TMA store
 //   warps 16-23 the state, fp32 in registers (a thread has half a row of R^T): R = e^{c_C} R + KV, split
+//   warp 24     loads (TMA, four stages of X, Y, Z)
+//   warp 25     issues KV_i and QK_{i+1}
+//   warp 26     issues O_i (one warp for all products spent longer on waits and issue than they take)
 // Instruction fetch bounds such a kernel as soon as the roles' loops outgrow the SM's instruction cache:
 // loop bodies are kept short (rolled where registers allow), and waits sleep instead of polling.
 // Infinities and NaN: masked entries of P are selected, not multiplied, but 0 * NaN in Z^T P^T would
@@ -50,7 +51,7 @@ namespace {
 
 using namespace lin;
 
-constexpr int NT = 768;
+constexpr int NT = 896;
 constexpr int NS = 4;                                 // load stages
 constexpr uint32_t SM_P = NS * STAGE;                 // P, two chunks' [64][64] bf16
 constexpr uint32_t SM_GATE = SM_P + 2 * 8192;
@@ -66,17 +67,21 @@ struct GateStage {
     short from[128];    // ... of channel j, first (backward: last) token
 };
 constexpr uint32_t SM_BAR = SM_GATE + NS * sizeof(GateStage);
-enum { B_FULL = 0, B_GATE = NS, B_EMPTY = 2 * NS, B_QKF = 3 * NS, B_QKE, B_PF, B_OF = B_PF + 2, B_KBF = B_OF + 2, B_ZF,
-       B_KVF, B_KVE, B_SF, B_SE, B_OE, B_DRAIN, NBAR };
+enum { B_FULL = 0, B_GATE = NS, B_EMPTY = 2 * NS, B_QKF = 3 * NS, B_QKE, B_PZ, B_OF = B_PZ + 2, B_KB = B_OF + 2,
+       B_KVF, B_S, B_SE, B_DRAIN, NBAR = B_DRAIN + 2 };
+// full: a stage's tiles; gate: its decays; empty: it may be loaded again; QKF, KVF, SE, OF: QK, KV, the state's product,
+// O are complete; QKE: QK is read; and what an MMA needs, all of it on one barrier (a wait costs the issuing
+// warp some 200 cycles even when it is over): PZ: P and Z^T for Z^T P^T; KB: Z^T's parts, and KV read, for KV;
+// S: the state's parts, and O read, for the state's product
 constexpr uint32_t SM_MISC = SM_BAR + NBAR * 8;       // tensor-memory address, abort flag
 constexpr uint32_t SM_ALLOC = SM_MISC + 16 + 1024;
 static_assert(SM_ALLOC <= 232448, "shared memory budget");
 
 constexpr long long NARROW = 96ll << 32;   // leaves x . y 31 binary orders before e^{-c_s} (x . y) overflows
 
-// registers of the six warpgroups: what they give up or take adds up to the launch's 80 each
-constexpr int RG_P = 72, RG_Z = 72, RG_OUT = 56, RG_STATE = 104;
-static_assert(RG_P + 2 * RG_Z + RG_OUT + 2 * RG_STATE <= 6 * 80, "more registers than the block has");
+// registers of the seven warpgroups: what they give up or take adds up to the launch's 72 each
+constexpr int RG_P = 72 /* the launch's own */, RG_Z = 64, RG_OUT = 56, RG_STATE = 104, RG_MMA = 40;
+static_assert(RG_P + 2 * RG_Z + RG_OUT + 2 * RG_STATE + RG_MMA <= 7 * 72, "more registers than the block has");
 
 // tensor-memory columns: KV, O, QK, the state's two parts, the scaled Z^T's three, Z^T
 constexpr uint32_t TM_KV = 0, TM_O = 128, TM_QK = 192, TM_S = 256, TM_ZP = 384, TM_Z = 480, TM_COLS = 512;
@@ -116,22 +121,19 @@ __global__ void __launch_bounds__(NT, 1) lin_chunk_kernel(const __grid_constant_
         for (int s = 0; s < NS; ++s) {
             mbar_init(bar + B_FULL + s, 1);
             mbar_init(bar + B_GATE + s, 1);
-            mbar_init(bar + B_EMPTY + s, 1 + 2 * JW + (STATE ? 0 : 4));   // products, state, outputs
+            mbar_init(bar + B_EMPTY + s, STATE ? 1 + 2 * JW : 2 + 2 * JW + 4);   // products, state, outputs
         }
         mbar_init(bar + B_QKF, 1);
         mbar_init(bar + B_QKE, 2);
         for (int s = 0; s < 2; ++s) {
-            mbar_init(bar + B_PF + s, 2);
+            mbar_init(bar + B_PZ + s, 2 + 8);
             mbar_init(bar + B_OF + s, 1);
+            mbar_init(bar + B_DRAIN + s, 1);
         }
-        mbar_init(bar + B_KBF, 8);
-        mbar_init(bar + B_ZF, 8);
+        mbar_init(bar + B_KB, 8 + 2 * JW);
         mbar_init(bar + B_KVF, 1);
-        mbar_init(bar + B_KVE, 2 * JW);
-        mbar_init(bar + B_SF, 2 * JW);
+        mbar_init(bar + B_S, 2 * JW + JW);
         mbar_init(bar + B_SE, 1);
-        mbar_init(bar + B_OE, JW);
-        mbar_init(bar + B_DRAIN, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     tc_fence_before();
@@ -143,7 +145,6 @@ __global__ void __launch_bounds__(NT, 1) lin_chunk_kernel(const __grid_constant_
     auto chunk = [&](int i) { return work.c0 + (rev ? nch - 1 - i : i); };
 
     if (wg == 0) {
-        regs_dec<RG_P>();
         if (warp < 2) {
           if constexpr (!STATE) {
             // ---- P: row r of QK
@@ -205,11 +206,11 @@ __global__ void __launch_bounds__(NT, 1) lin_chunk_kernel(const __grid_constant_
                 tc_fence_before();
                 warp_arrive(bar + B_QKE);
                 fence_async_smem();
-                warp_arrive(bar + B_PF + pb);
+                warp_arrive(bar + B_PZ + pb);
             }
           }
         } else if (warp == 2) {
-            // ---- loads and decays (a chunk's log-decays are on their way while the one before is summed)
+            // ---- decays (a chunk's are on their way while the one before is summed)
             float next[2] = {0.f, 0.f};
             auto gate_load = [&](int i) {
                 const int t0 = chunk(i) * C;
@@ -222,22 +223,9 @@ __global__ void __launch_bounds__(NT, 1) lin_chunk_kernel(const __grid_constant_
             if (nch > 0) gate_load(0);
             long long sum = 0;   // of the segment's log-decays
             bool any_nan = false;
-            int i = 0;
-            for (; i < nch; ++i) {
+            for (int i = 0; i < nch; ++i) {
                 const int s = i % NS, t0 = chunk(i) * C;
                 if (i >= NS && !wait(bar + B_EMPTY + s, (i / NS - 1) & 1, s_abort)) break;
-                if (lane == 0) {
-                    uint8_t *st = sm + s * STAGE;
-                    mbar_expect_tx(bar + B_FULL + s, ((STATE ? 1 : 2) * DX + DZ) * C * 2);
-#pragma unroll
-                    for (int p = 0; p < DX / 64; ++p) {
-                        if (!STATE) tma_load_3d(st + p * 8192, &P.tx, bar + B_FULL + s, p * 64, h / a.gx, row0 + t0);
-                        tma_load_3d(st + TILE + p * 8192, &P.ty, bar + B_FULL + s, p * 64, h / a.gy, row0 + t0);
-                    }
-#pragma unroll
-                    for (int p = 0; p < DZ / 64; ++p)
-                        tma_load_3d(st + 2 * TILE + p * 8192, &P.tz, bar + B_FULL + s, p * 64, h / a.gz, row0 + t0);
-                }
                 GateStage &G = gates[s];
                 // e^g is 0 far before -10^4 (and infinite before 10^4, which breaks the contract)
                 const float ga = fminf(fmaxf(next[0], -1e4f), 1e4f), gb = fminf(fmaxf(next[1], -1e4f), 1e4f);
@@ -284,73 +272,6 @@ __global__ void __launch_bounds__(NT, 1) lin_chunk_kernel(const __grid_constant_
             }
             if (STATE && lane == 0)
                 a.seg_total[(size_t)work.slot * a.H + h] = any_nan ? __int_as_float(0x7fc00000) : fix_exp2(sum);
-            // no load is in flight when the CTA ends, wound down early or not
-            if (lane == 0)
-                for (int j = max(0, i - NS); j < i; ++j) mbar_wait_cycles(bar + B_FULL + j % NS, (j / NS) & 1, WAIT_LIMIT);
-        } else {
-            // ---- MMA issue
-            const uint32_t lead = lane == 0;
-            constexpr uint32_t ID_QK = idesc_bf16(128, C, false, false), ID_KV = idesc_bf16(128, DX, false, true);
-            constexpr uint32_t ID_O = idesc_bf16(128, C, false, false);
-            const uint32_t pt = k_tile(sb + SM_P);
-            bool ok = true;
-            for (int i = -1; i < nch && ok; ++i) {
-                const uint32_t st = sb + ((i + NS) % NS) * STAGE;
-                if (i >= 0) {
-                    ok = wait(bar + B_KBF, i & 1, s_abort) && (i == 0 || wait(bar + B_KVE, (i - 1) & 1, s_abort));
-                    if (!ok) break;
-                    tc_fence_after();
-                    const uint32_t y = mn_tile(st + TILE);
-#pragma unroll 1
-                    for (int p = 0; p < 3; ++p)
-#pragma unroll
-                        for (int kk = 0; kk < C / 16; ++kk)
-                            mma_bf16_ts_warp(tbase + TM_KV, tbase + TM_ZP + p * 32 + kk * 8, dMN(y, kk), ID_KV, p + kk > 0, lead);
-                    mma_commit_warp(bar + B_KVF, lead);
-                    if (STATE) mma_commit_warp(bar + B_EMPTY + i % NS, lead);
-                }
-                if (!STATE && i + 1 < nch) {   // QK of the next one; rows 64-127 of A are what lies behind X: lanes nobody reads
-                    const int sn = (i + 1) % NS;
-                    const uint32_t x = k_tile(sb + sn * STAGE), y = k_tile(sb + sn * STAGE + TILE);
-                    ok = wait(bar + B_FULL + sn, ((i + 1) / NS) & 1, s_abort) &&
-                         (i < 0 || wait(bar + B_QKE, i & 1, s_abort));
-                    if (!ok) break;
-                    tc_fence_after();
-#pragma unroll 1
-                    for (int p = 0; p < DX / 64; ++p)
-#pragma unroll
-                        for (int kk = 0; kk < 4; ++kk)
-                            mma_bf16_warp(tbase + TM_QK, dK(x, kk) + p * 512, dK(y, kk) + p * 512, ID_QK, p + kk > 0, lead);
-                    mma_commit_warp(bar + B_QKF, lead);
-                }
-                if (STATE || i < 0) continue;
-                ok = wait(bar + B_SF, i & 1, s_abort) && (i == 0 || wait(bar + B_OE, (i - 1) & 1, s_abort));
-                if (!ok) break;
-                tc_fence_after();
-                const uint32_t x = k_tile(st);
-#pragma unroll 1
-                for (int p = 0; p < 2 * (DX / 64); ++p) {   // a part's panel of 64 key channels
-                    const int part = p / (DX / 64), panel = p % (DX / 64);
-#pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        mma_bf16_ts_warp(tbase + TM_O, tbase + TM_S + part * 64 + panel * 32 + kk * 8, dK(x, kk) + panel * 512,
-                                         ID_O, p + kk > 0, lead);
-                }
-                mma_commit_warp(bar + B_SE, lead);
-                ok = wait(bar + B_PF + (i & 1), (i >> 1) & 1, s_abort) && wait(bar + B_ZF, i & 1, s_abort);
-                if (!ok) break;
-                tc_fence_after();
-#pragma unroll
-                for (int kk = 0; kk < C / 16; ++kk)
-                    mma_bf16_ts_warp(tbase + TM_O, tbase + TM_Z + kk * 8, dK(pt + (i & 1) * 512, kk), ID_O, 1, lead);
-                mma_commit_warp(bar + B_OF + (i & 1), lead);
-                mma_commit_warp(bar + B_EMPTY + i % NS, lead);
-            }
-            // products still running are waited for below (every product of a full run is, by its readers)
-            if (!ok) {
-                mma_commit_warp(bar + B_DRAIN, lead);
-                if (lane == 0) mbar_wait_cycles(bar + B_DRAIN, 0, WAIT_LIMIT);
-            }
         }
     } else if (wg <= 2) {
         regs_dec<RG_Z>();
@@ -457,7 +378,7 @@ __global__ void __launch_bounds__(NT, 1) lin_chunk_kernel(const __grid_constant_
                 tmem_wait_st();
                 tc_fence_before();
             }
-            warp_arrive(bar + B_KBF);
+            warp_arrive(bar + B_KB);
             if (STATE) continue;
             // Z^T itself: O_{i-1} has read the last one
             if (i > 0) ok = ok && wait(bar + B_OF + ((i - 1) & 1), ((i - 1) >> 1) & 1, s_abort);
@@ -469,7 +390,7 @@ __global__ void __launch_bounds__(NT, 1) lin_chunk_kernel(const __grid_constant_
                 tmem_wait_st();
                 tc_fence_before();
             }
-            warp_arrive(bar + B_ZF);
+            warp_arrive(bar + B_PZ + (i & 1));
         }
     } else if (wg == 3) {
         regs_dec<RG_OUT>();
@@ -480,6 +401,7 @@ __global__ void __launch_bounds__(NT, 1) lin_chunk_kernel(const __grid_constant_
         const size_t ld = (size_t)a.H * DZ;
         const int q = warp & 3;
         bool ok = true;
+        if (q < JW) warp_arrive(bar + B_S);   // O has nothing to be read yet
         for (int i = 0; i < nch; ++i) {
             const int s = i % NS, t0 = chunk(i) * C;
             ok = wait(bar + B_OF + (i & 1), (i >> 1) & 1, s_abort);
@@ -499,7 +421,7 @@ __global__ void __launch_bounds__(NT, 1) lin_chunk_kernel(const __grid_constant_
                     tmem_wait_ld();
                     if (x == 3) {   // the accumulator is read
                         tc_fence_before();
-                        warp_arrive(bar + B_OE);
+                        warp_arrive(bar + B_S);
                     }
                     if (narrow) {
 #pragma unroll
@@ -550,7 +472,7 @@ __global__ void __launch_bounds__(NT, 1) lin_chunk_kernel(const __grid_constant_
         }
         bulk_wait_all();
       }
-    } else {
+    } else if (wg <= 5) {
         regs_inc<RG_STATE>();
         // ---- state: row j of R^T, half of its columns
         constexpr int CX = DX / 2;
@@ -572,6 +494,7 @@ __global__ void __launch_bounds__(NT, 1) lin_chunk_kernel(const __grid_constant_
                 for (int e = 0; e < CX / 2; ++e) S[e] = make_float2(0.f, 0.f);
             }
             bool ok = true;
+            warp_arrive(bar + B_KB);   // KV has nothing to be read yet
             // iteration i: the state before it is published (and written where it is a boundary's or the last)
             for (int i = 0;; ++i) {
                 if ((!STATE && a.snap) || i == nch) {
@@ -616,7 +539,7 @@ __global__ void __launch_bounds__(NT, 1) lin_chunk_kernel(const __grid_constant_
                 }
                 tmem_wait_st();
                 tc_fence_before();
-                warp_arrive(bar + B_SF);
+                warp_arrive(bar + B_S);
               }
                 const int s = i % NS;
                 ok = wait(bar + B_KVF, i & 1, s_abort);
@@ -634,7 +557,7 @@ __global__ void __launch_bounds__(NT, 1) lin_chunk_kernel(const __grid_constant_
                         S[b * 8 + e] = __ffma2_rn(S[b * 8 + e], tot, make_float2(v[2 * e], v[2 * e + 1]));
                 }
                 tc_fence_before();
-                warp_arrive(bar + B_KVE);
+                warp_arrive(bar + B_KB);
                 if (G.bad && G.from[j] >= 0 && G.from[j] < C) {
 #pragma unroll
                     for (int e = 0; e < CX / 2; ++e) S[e] = make_float2(__int_as_float(0x7fc00000), __int_as_float(0x7fc00000));
@@ -643,6 +566,94 @@ __global__ void __launch_bounds__(NT, 1) lin_chunk_kernel(const __grid_constant_
             }
             if (!ok && s_out)
                 for (int e = 0; e < CX; ++e) s_out[(size_t)(i0 + e) * DZ + j] = __int_as_float(0x7fc00000);
+        }
+    } else {
+        regs_dec<RG_MMA>();
+        const uint32_t lead = lane == 0;
+        bool ok = true;
+        if (warp == 24) {
+            // ---- loads
+            int i = 0;
+            for (; i < nch; ++i) {
+                const int s = i % NS, t0 = chunk(i) * C;
+                if (i >= NS && !wait(bar + B_EMPTY + s, (i / NS - 1) & 1, s_abort)) break;
+                if (lane == 0) {
+                    uint8_t *st = sm + s * STAGE;
+                    mbar_expect_tx(bar + B_FULL + s, ((STATE ? 1 : 2) * DX + DZ) * C * 2);
+#pragma unroll
+                    for (int p = 0; p < DX / 64; ++p) {
+                        if (!STATE) tma_load_3d(st + p * 8192, &P.tx, bar + B_FULL + s, p * 64, h / a.gx, row0 + t0);
+                        tma_load_3d(st + TILE + p * 8192, &P.ty, bar + B_FULL + s, p * 64, h / a.gy, row0 + t0);
+                    }
+#pragma unroll
+                    for (int p = 0; p < DZ / 64; ++p)
+                        tma_load_3d(st + 2 * TILE + p * 8192, &P.tz, bar + B_FULL + s, p * 64, h / a.gz, row0 + t0);
+                }
+            }
+            // no load is in flight when the CTA ends, wound down early or not
+            if (lane == 0)
+                for (int j = max(0, i - NS); j < i; ++j) mbar_wait_cycles(bar + B_FULL + j % NS, (j / NS) & 1, WAIT_LIMIT);
+        } else if (warp == 25) {
+            // ---- KV_i and QK_{i+1}
+            constexpr uint32_t ID_QK = idesc_bf16(128, C, false, false), ID_KV = idesc_bf16(128, DX, false, true);
+            for (int i = -1; i < nch && ok; ++i) {
+                if (i >= 0) {
+                    ok = wait(bar + B_KB, i & 1, s_abort);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t y = mn_tile(sb + i % NS * STAGE + TILE);
+#pragma unroll 1
+                    for (int p = 0; p < 3; ++p)
+#pragma unroll
+                        for (int kk = 0; kk < C / 16; ++kk)
+                            mma_bf16_ts_warp(tbase + TM_KV, tbase + TM_ZP + p * 32 + kk * 8, dMN(y, kk), ID_KV, p + kk > 0, lead);
+                    mma_commit_warp(bar + B_KVF, lead);
+                    mma_commit_warp(bar + B_EMPTY + i % NS, lead);
+                }
+                if (!STATE && i + 1 < nch) {   // rows 64-127 of A are what lies behind X: lanes nobody reads
+                    const int sn = (i + 1) % NS;
+                    const uint32_t x = k_tile(sb + sn * STAGE), y = k_tile(sb + sn * STAGE + TILE);
+                    ok = wait(bar + B_FULL + sn, ((i + 1) / NS) & 1, s_abort) &&
+                         (i < 0 || wait(bar + B_QKE, i & 1, s_abort));
+                    if (!ok) break;
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int p = 0; p < DX / 64; ++p)
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+                            mma_bf16_warp(tbase + TM_QK, dK(x, kk) + p * 512, dK(y, kk) + p * 512, ID_QK, p + kk > 0, lead);
+                    mma_commit_warp(bar + B_QKF, lead);
+                }
+            }
+        } else if (!STATE && warp == 26) {
+            // ---- O_i: the state's product and the chunk's
+            constexpr uint32_t ID_O = idesc_bf16(128, C, false, false);
+            const uint32_t pt = k_tile(sb + SM_P);
+            for (int i = 0; i < nch; ++i) {
+                ok = wait(bar + B_PZ + (i & 1), (i >> 1) & 1, s_abort) && wait(bar + B_S, i & 1, s_abort);
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t x = k_tile(sb + i % NS * STAGE);
+#pragma unroll 1
+                for (int p = 0; p < 2 * (DX / 64); ++p) {   // a part's panel of 64 key channels
+                    const int part = p / (DX / 64), panel = p % (DX / 64);
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        mma_bf16_ts_warp(tbase + TM_O, tbase + TM_S + part * 64 + panel * 32 + kk * 8, dK(x, kk) + panel * 512,
+                                         ID_O, p + kk > 0, lead);
+                }
+                mma_commit_warp(bar + B_SE, lead);
+#pragma unroll
+                for (int kk = 0; kk < C / 16; ++kk)
+                    mma_bf16_ts_warp(tbase + TM_O, tbase + TM_Z + kk * 8, dK(pt + (i & 1) * 512, kk), ID_O, 1, lead);
+                mma_commit_warp(bar + B_OF + (i & 1), lead);
+                mma_commit_warp(bar + B_EMPTY + i % NS, lead);
+            }
+        }
+        // products still running are waited for here (every product of a full run is, by its readers)
+        if (!ok && (warp == 25 || warp == 26)) {
+            mma_commit_warp(bar + B_DRAIN + warp - 25, lead);
+            if (lane == 0) mbar_wait_cycles(bar + B_DRAIN + warp - 25, 0, WAIT_LIMIT);
         }
     }
     tc_fence_before();
