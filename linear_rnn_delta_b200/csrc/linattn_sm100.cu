@@ -157,51 +157,56 @@ __global__ void __launch_bounds__(NT, 1) lin_chunk_kernel(const __grid_constant_
                     (i >= 2 && !wait(bar + B_OF + pb, ((i >> 1) - 1) & 1, s_abort)))
                     break;
                 tc_fence_after();
-                const int first = rev ? r : 0, last = rev ? G.nv - 1 : r;   // the row's tokens
-                const float2 cr = G.c[r];
                 const bool narrow = G.narrow != 0;
                 uint8_t *prow = sm + SM_P + pb * 8192 + r * 128;
 #pragma unroll 1
                 for (int half = 0; half < 2; ++half) {
-                    uint32_t pk[16];
-                    if (rev ? half < warp : half > warp) {   // masked for all of the warp's rows
+                    // the row's tokens among these 32, as bits: s <= r, or backward r <= s < nv
+                    const int lo = rev ? r - half * 32 : 0, hi = (rev ? G.nv - 1 : r) - half * 32;
+                    uint32_t keep = hi < 0 || lo > 31 ? 0u : 0xffffffffu >> (31 - min(hi, 31));
+                    if (lo > 0 && lo <= 31) keep &= 0xffffffffu << lo;
+                    if (rev ? half < warp : half > warp) {   // nobody's
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) pk[e] = 0u;
-                    } else {
+                        for (int q = 0; q < 4; ++q)
+                            *reinterpret_cast<uint4 *>(prow + (((half * 4 + q) ^ (r & 7)) << 4)) = make_uint4(0, 0, 0, 0);
+                    } else if (narrow) {
                         float2 v[16];
+                        uint32_t pk[16];
                         tmem_ld32(tlane + TM_QK + half * 32, &v[0].x);
                         tmem_wait_ld();
-                        if (narrow) {
 #pragma unroll
-                            for (int e = 0; e < 16; e += 2) {
-                                const float4 bs = *reinterpret_cast<const float4 *>(&G.b[half * 32 + 2 * e]);
-                                v[e] = __fmul2_rn(v[e], make_float2(bs.x, bs.y));
-                                v[e + 1] = __fmul2_rn(v[e + 1], make_float2(bs.z, bs.w));
-                            }
-                        } else {   // a strong decay or a reset in the chunk: each pair's own exponential
-#pragma unroll
-                            for (int e = 0; e < 16; ++e) {
-                                const float4 cs = *reinterpret_cast<const float4 *>(&G.c[half * 32 + 2 * e]);
-                                const float d0 = diff(cr, make_float2(cs.x, cs.y)), d1 = diff(cr, make_float2(cs.z, cs.w));
-                                v[e].x *= ex2(rev ? -d0 : d0);
-                                v[e].y *= ex2(rev ? -d1 : d1);
-                            }
-                        }
-                        if (half == warp || (rev && G.nv < C)) {   // columns that some row of the warp masks
-#pragma unroll
-                            for (int e = 0; e < 16; ++e) {
-                                const int s0 = half * 32 + 2 * e;
-                                if (s0 < first || s0 > last) v[e].x = 0.f;
-                                if (s0 + 1 < first || s0 + 1 > last) v[e].y = 0.f;
-                            }
+                        for (int e = 0; e < 16; e += 2) {
+                            const float4 bs = *reinterpret_cast<const float4 *>(&G.b[half * 32 + 2 * e]);
+                            v[e] = __fmul2_rn(v[e], make_float2(bs.x, bs.y));
+                            v[e + 1] = __fmul2_rn(v[e + 1], make_float2(bs.z, bs.w));
                         }
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) pk[e] = pack_bf16(v[e].x, v[e].y);
+                        for (int e = 0; e < 16; ++e) {
+                            if (!(keep & (1u << (2 * e)))) v[e].x = 0.f;
+                            if (!(keep & (2u << (2 * e)))) v[e].y = 0.f;
+                            pk[e] = pack_bf16(v[e].x, v[e].y);
+                        }
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            *reinterpret_cast<uint4 *>(prow + (((half * 4 + q) ^ (r & 7)) << 4)) =
+                                make_uint4(pk[4 * q], pk[4 * q + 1], pk[4 * q + 2], pk[4 * q + 3]);
+                    } else {   // a strong decay or a reset in the chunk: each pair's own exponential
+                        const float2 cr = G.c[r];
+#pragma unroll 1
+                        for (int q = 0; q < 4; ++q, keep >>= 8) {
+                            float v[8];
+                            tmem_ld8(tlane + TM_QK + half * 32 + q * 8, v);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) {
+                                const float d = diff(cr, G.c[half * 32 + q * 8 + e]);
+                                v[e] = keep & (1u << e) ? v[e] * ex2(rev ? -d : d) : 0.f;
+                            }
+                            *reinterpret_cast<uint4 *>(prow + (((half * 4 + q) ^ (r & 7)) << 4)) =
+                                make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]),
+                                           pack_bf16(v[6], v[7]));
+                        }
                     }
-#pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        *reinterpret_cast<uint4 *>(prow + (((half * 4 + q) ^ (r & 7)) << 4)) =
-                            make_uint4(pk[4 * q], pk[4 * q + 1], pk[4 * q + 2], pk[4 * q + 3]);
                 }
                 tc_fence_before();
                 warp_arrive(bar + B_QKE);
@@ -293,12 +298,11 @@ __global__ void __launch_bounds__(NT, 1) lin_chunk_kernel(const __grid_constant_
             const int nv = G.nv;
             // rows of Y and Z behind the sequence's end belong to another one (or hold nothing): zero
             if (nv < C) {
-                const int rest = (C - nv) * 8;
+                const int p = (t & 31) >> 3;   // panel: Y's, then Z's
+                if (p < 2 ? p < DX / 64 : p - 2 < DZ / 64) {
 #pragma unroll 1
-                for (int e = t; e < (DX / 64 + DZ / 64) * rest; e += ZT) {
-                    const int p = e / rest;
-                    *reinterpret_cast<uint4 *>(st + TILE + (p < DX / 64 ? p : p - DX / 64 + 2) * 8192 + nv * 128 +
-                                               e % rest * 16) = make_uint4(0, 0, 0, 0);
+                    for (int r = nv + (t >> 5); r < C; r += ZT / 32)
+                        *reinterpret_cast<uint4 *>(st + TILE + p * 8192 + r * 128 + (t & 7) * 16) = make_uint4(0, 0, 0, 0);
                 }
                 fence_async_smem();
                 group_sync(1, ZT);
@@ -478,23 +482,28 @@ __global__ void __launch_bounds__(NT, 1) lin_chunk_kernel(const __grid_constant_
         constexpr int CX = DX / 2;
         if ((warp & 3) < JW) {
             const int j = (warp & 3) * 32 + lane, i0 = (wg - 4) * CX;
-            float2 S[CX / 2];
             const float *s_in = STATE ? nullptr : a.seg_chunks ? a.seg_state + woff : a.s_in ? a.s_in + soff : nullptr;
             float *s_out = STATE ? a.seg_state + woff : a.s_out && closing ? a.s_out + soff : nullptr;
-            if (s_in && a.in_t && !a.seg_chunks) {
+            // between memory and the registers by way of the tensor memory that KV has later: short loops
+            const uint32_t scratch = tlane + TM_KV + i0;
+            {
+                const bool t = s_in && a.in_t && !a.seg_chunks;
+                const float *at = s_in + (t ? (size_t)j * DX + i0 : (size_t)i0 * DZ + j);
+                const int step = t ? 1 : DZ;
+#pragma unroll 1
+                for (int b = 0; b < CX / 16; ++b, at += 16 * step) {
+                    float v[16];
 #pragma unroll
-                for (int e = 0; e < CX / 2; ++e)
-                    S[e] = *reinterpret_cast<const float2 *>(s_in + (size_t)j * DX + i0 + 2 * e);
-            } else if (s_in) {
-                const float *at = s_in + (size_t)i0 * DZ + j;
-#pragma unroll
-                for (int e = 0; e < CX / 2; ++e) S[e] = make_float2(at[2 * e * DZ], at[(2 * e + 1) * DZ]);
-            } else {
-#pragma unroll
-                for (int e = 0; e < CX / 2; ++e) S[e] = make_float2(0.f, 0.f);
+                    for (int e = 0; e < 16; ++e) v[e] = s_in ? at[e * step] : 0.f;
+                    tmem_st16(scratch + b * 16, v);
+                }
+                tmem_wait_st();
             }
+            float2 S[CX / 2];
+#pragma unroll
+            for (int b = 0; b < CX / 16; ++b) tmem_ld16(scratch + b * 16, &S[b * 8].x);
+            tmem_wait_ld();
             bool ok = true;
-            warp_arrive(bar + B_KB);   // KV has nothing to be read yet
             // iteration i: the state before it is published (and written where it is a boundary's or the last)
             for (int i = 0;; ++i) {
                 if ((!STATE && a.snap) || i == nch) {
@@ -506,41 +515,49 @@ __global__ void __launch_bounds__(NT, 1) lin_chunk_kernel(const __grid_constant_
                     if (!STATE && a.snap && edge >= 0 && (edge == len - 1 || (edge + 1) % a.snap_tokens == 0))
                         to[0] = a.snap + ((size_t)(n + row0 / a.snap_tokens + edge / a.snap_tokens) * a.H + h) * DX * DZ;
                     if (i == nch) to[1] = s_out;
-#pragma unroll 1
-                    for (int w = 0; w < 2; ++w) {
-                        float *dst = w ? to[1] : to[0];
-                        if (!dst) continue;
-                        dst += (size_t)i0 * DZ + j;
+                    if (to[0] || to[1]) {
 #pragma unroll
-                        for (int e = 0; e < CX / 2; ++e) {
-                            dst[2 * e * DZ] = S[e].x;
-                            dst[(2 * e + 1) * DZ] = S[e].y;
+                        for (int b = 0; b < CX / 16; ++b) tmem_st16(scratch + b * 16, &S[b * 8].x);
+                        tmem_wait_st();
+#pragma unroll 1
+                        for (int b = 0; b < CX / 8; ++b) {   // half of them for the second destination
+                            float v[16];
+                            float *dst = b < CX / 16 ? to[0] : to[1];
+                            if (!dst) continue;
+                            const int b16 = (b & (CX / 16 - 1)) * 16;
+                            tmem_ld16(scratch + b16, v);
+                            tmem_wait_ld();
+                            dst += (size_t)(i0 + b16) * DZ + j;
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) dst[e * DZ] = v[e];
                         }
                     }
                     if (i == nch) break;
                 }
-              if constexpr (!STATE) {
-                if (i > 0) {
-                    ok = wait(bar + B_SE, (i - 1) & 1, s_abort);   // O_{i-1} has read the parts
-                    if (!ok) break;
-                    tc_fence_after();
-                }
-#pragma unroll
-                for (int b = 0; b < CX / 16; ++b) {
-                    uint32_t hi[8], lo[8];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        float2 x = S[b * 8 + e];
-                        hi[e] = take_part(x);
-                        lo[e] = pack_bf16(x.x, x.y);
-                    }
-                    tmem_st8(tlane + TM_S + i0 / 2 + b * 8, hi);
-                    tmem_st8(tlane + TM_S + 64 + i0 / 2 + b * 8, lo);
-                }
-                tmem_wait_st();
                 tc_fence_before();
-                warp_arrive(bar + B_S);
-              }
+                warp_arrive(bar + B_KB);   // KV is read (the first time there is nothing to be read)
+                if constexpr (!STATE) {
+                    if (i > 0) {
+                        ok = wait(bar + B_SE, (i - 1) & 1, s_abort);   // O_{i-1} has read the parts
+                        if (!ok) break;
+                        tc_fence_after();
+                    }
+#pragma unroll
+                    for (int b = 0; b < CX / 16; ++b) {
+                        uint32_t hi[8], lo[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            float2 x = S[b * 8 + e];
+                            hi[e] = take_part(x);
+                            lo[e] = pack_bf16(x.x, x.y);
+                        }
+                        tmem_st8(tlane + TM_S + i0 / 2 + b * 8, hi);
+                        tmem_st8(tlane + TM_S + 64 + i0 / 2 + b * 8, lo);
+                    }
+                    tmem_wait_st();
+                    tc_fence_before();
+                    warp_arrive(bar + B_S);
+                }
                 const int s = i % NS;
                 ok = wait(bar + B_KVF, i & 1, s_abort);
                 if (!ok) break;
@@ -550,14 +567,12 @@ __global__ void __launch_bounds__(NT, 1) lin_chunk_kernel(const __grid_constant_
 #pragma unroll
                 for (int b = 0; b < CX / 16; ++b) {
                     float v[16];
-                    tmem_ld16(tlane + TM_KV + i0 + b * 16, v);
+                    tmem_ld16(scratch + b * 16, v);
                     tmem_wait_ld();
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
                         S[b * 8 + e] = __ffma2_rn(S[b * 8 + e], tot, make_float2(v[2 * e], v[2 * e + 1]));
                 }
-                tc_fence_before();
-                warp_arrive(bar + B_KB);
                 if (G.bad && G.from[j] >= 0 && G.from[j] < C) {
 #pragma unroll
                     for (int e = 0; e < CX / 2; ++e) S[e] = make_float2(__int_as_float(0x7fc00000), __int_as_float(0x7fc00000));
@@ -565,6 +580,7 @@ __global__ void __launch_bounds__(NT, 1) lin_chunk_kernel(const __grid_constant_
                 warp_arrive(bar + B_EMPTY + s);
             }
             if (!ok && s_out)
+#pragma unroll 1
                 for (int e = 0; e < CX; ++e) s_out[(size_t)(i0 + e) * DZ + j] = __int_as_float(0x7fc00000);
         }
     } else {
@@ -573,6 +589,7 @@ __global__ void __launch_bounds__(NT, 1) lin_chunk_kernel(const __grid_constant_
         bool ok = true;
         if (warp == 24) {
             // ---- loads
+            const int hx = h / a.gx, hy = h / a.gy, hz = h / a.gz;
             int i = 0;
             for (; i < nch; ++i) {
                 const int s = i % NS, t0 = chunk(i) * C;
@@ -582,12 +599,12 @@ __global__ void __launch_bounds__(NT, 1) lin_chunk_kernel(const __grid_constant_
                     mbar_expect_tx(bar + B_FULL + s, ((STATE ? 1 : 2) * DX + DZ) * C * 2);
 #pragma unroll
                     for (int p = 0; p < DX / 64; ++p) {
-                        if (!STATE) tma_load_3d(st + p * 8192, &P.tx, bar + B_FULL + s, p * 64, h / a.gx, row0 + t0);
-                        tma_load_3d(st + TILE + p * 8192, &P.ty, bar + B_FULL + s, p * 64, h / a.gy, row0 + t0);
+                        if (!STATE) tma_load_3d(st + p * 8192, &P.tx, bar + B_FULL + s, p * 64, hx, row0 + t0);
+                        tma_load_3d(st + TILE + p * 8192, &P.ty, bar + B_FULL + s, p * 64, hy, row0 + t0);
                     }
 #pragma unroll
                     for (int p = 0; p < DZ / 64; ++p)
-                        tma_load_3d(st + 2 * TILE + p * 8192, &P.tz, bar + B_FULL + s, p * 64, h / a.gz, row0 + t0);
+                        tma_load_3d(st + 2 * TILE + p * 8192, &P.tz, bar + B_FULL + s, p * 64, hz, row0 + t0);
                 }
             }
             // no load is in flight when the CTA ends, wound down early or not
@@ -602,11 +619,9 @@ __global__ void __launch_bounds__(NT, 1) lin_chunk_kernel(const __grid_constant_
                     if (!ok) break;
                     tc_fence_after();
                     const uint32_t y = mn_tile(sb + i % NS * STAGE + TILE);
-#pragma unroll 1
-                    for (int p = 0; p < 3; ++p)
-#pragma unroll
-                        for (int kk = 0; kk < C / 16; ++kk)
-                            mma_bf16_ts_warp(tbase + TM_KV, tbase + TM_ZP + p * 32 + kk * 8, dMN(y, kk), ID_KV, p + kk > 0, lead);
+#pragma unroll 2
+                    for (int k = 0; k < 3 * C / 16; ++k)   // the parts' columns follow one another
+                        mma_bf16_ts_warp(tbase + TM_KV, tbase + TM_ZP + k * 8, dMN(y, k & (C / 16 - 1)), ID_KV, k > 0, lead);
                     mma_commit_warp(bar + B_KVF, lead);
                     mma_commit_warp(bar + B_EMPTY + i % NS, lead);
                 }
@@ -617,11 +632,9 @@ __global__ void __launch_bounds__(NT, 1) lin_chunk_kernel(const __grid_constant_
                          (i < 0 || wait(bar + B_QKE, i & 1, s_abort));
                     if (!ok) break;
                     tc_fence_after();
-#pragma unroll 1
-                    for (int p = 0; p < DX / 64; ++p)
-#pragma unroll
-                        for (int kk = 0; kk < 4; ++kk)
-                            mma_bf16_warp(tbase + TM_QK, dK(x, kk) + p * 512, dK(y, kk) + p * 512, ID_QK, p + kk > 0, lead);
+#pragma unroll 2
+                    for (int k = 0; k < DX / 16; ++k)
+                        mma_bf16_warp(tbase + TM_QK, dK(x, k), dK(y, k), ID_QK, k > 0, lead);
                     mma_commit_warp(bar + B_QKF, lead);
                 }
             }
@@ -634,13 +647,10 @@ __global__ void __launch_bounds__(NT, 1) lin_chunk_kernel(const __grid_constant_
                 if (!ok) break;
                 tc_fence_after();
                 const uint32_t x = k_tile(sb + i % NS * STAGE);
-#pragma unroll 1
-                for (int p = 0; p < 2 * (DX / 64); ++p) {   // a part's panel of 64 key channels
-                    const int part = p / (DX / 64), panel = p % (DX / 64);
-#pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        mma_bf16_ts_warp(tbase + TM_O, tbase + TM_S + part * 64 + panel * 32 + kk * 8, dK(x, kk) + panel * 512,
-                                         ID_O, p + kk > 0, lead);
+#pragma unroll 4
+                for (int k = 0; k < 2 * DX / 16; ++k) {   // both parts
+                    const int kk = k & (DX / 16 - 1);
+                    mma_bf16_ts_warp(tbase + TM_O, tbase + TM_S + (k / (DX / 16)) * 64 + kk * 8, dK(x, kk), ID_O, k > 0, lead);
                 }
                 mma_commit_warp(bar + B_SE, lead);
 #pragma unroll

@@ -99,7 +99,7 @@ __device__ __forceinline__ long long fix_log2(float g)
     // g log2(e) as two floats: the rounding of the product, and of log2(e), would show in long sums
     const float hi = g * 1.44269502f, lo = fmaf(g, 1.44269502f, -hi) + g * 1.92596303e-8f;
     const float n = rintf(hi);
-    return ((long long)(int)n << 32) + (long long)__float2ll_rn(((hi - n) + lo) * 4294967296.f);
+    return ((long long)(int)n << 32) + (long long)__float2int_rn(((hi - n) + lo) * 4294967296.f);
 }
 // integer part and rest in [-1/2, 1/2)
 __device__ __forceinline__ int fix_int(long long x) { return (int)((x + 0x80000000ll) >> 32); }
