@@ -44,21 +44,18 @@ __device__ __forceinline__ int lin_len(const LinRun &a, int n)
     return a.cu_seqlens ? a.cu_seqlens[n + 1] - a.cu_seqlens[n] : a.T;
 }
 
-// Tokens between the state boundaries that the gate gradient restarts its sums from.
-constexpr int LIN_SEG = 512;
-
-// Arguments of the backward's closing kernels.
+// Arguments of the gate gradient's kernels.
 struct LinGateGrad {
-    const float *dot_q, *dot_k;     // [H][rows]: q.dq and k.dk of every token
-    const float *snap_s, *snap_g;   // boundary states of the dq and dk passes [slot][H][dv][dk]
-    const float *g;                 // log-decays as in LinRun: dg is 0 where the decay is
+    const void *q, *k, *v, *d_o;
+    const float *snap_s, *snap_g;   // the dq and dk passes' states at boundaries of 64 tokens [slot][H][dv][dk]
+    const float *s_init, *g_end;    // initial state and dL/dS_final, [N][H][dk][dv] or NULL
+    const float *g;                 // log-decays as in LinRun
     int g_ld;
-    const float *g_end;             // dL/dS_final or NULL: the last boundary of a sequence counts only with it
     float *dg;                      // [rows][H], or NULL with a decay of each head
-    float *partial;                 // [slot][H] sums over a segment's tokens (decay of each head), or NULL
+    float *partial;                 // [slot][H] sums over a chunk's tokens (decay of each head), or NULL
     float *dg_head;                 // [H]
     long long rows;
-    int H, dk, dv, num_seqs, T, slots;
+    int Hk, H, dk, dv, num_seqs, T, slots;
     const int32_t *cu_seqlens;
 };
 
@@ -75,12 +72,11 @@ bool lin_chunk_takes(int dx, int dz);
 cudaError_t launch_lin_states(const LinRun &r, int dx, int dz, cudaStream_t st);       // fills seg_state
 cudaError_t launch_lin_chunk(const LinRun &r, int dx, int dz, cudaStream_t st);        // bf16 outputs
 cudaError_t launch_lin_chunk_fine(const LinRun &r, int dx, int dz, cudaStream_t st);   // fp32 outputs
-// Sums the per-value-head fp32 gradients over the heads that share a key head, casts them, and
-// forms the dots.  dqf, dkf: [rows][H][dk]; dq, dk, q, k: [rows][Hk][dk].
-cudaError_t launch_lin_share(const float *dqf, const float *dkf, const void *q, const void *k, void *dq, void *dk,
-                             float *dot_q, float *dot_k, long long rows, int Hk, int H, int d_k, bool bf16,
-                             cudaStream_t st);
-cudaError_t launch_lin_gate_grad(const LinGateGrad &a, cudaStream_t st);
+// Sums the per-value-head fp32 gradients over the heads that share a key head and casts them: dqf, dkf
+// [rows][H][dk]; dq, dk [rows][Hk][dk].
+cudaError_t launch_lin_share(const float *dqf, const float *dkf, void *dq, void *dk, long long rows, int Hk, int H,
+                             int d_k, bool bf16, cudaStream_t st);
+cudaError_t launch_lin_gate_grad(const LinGateGrad &a, bool bf16, cudaStream_t st);
 
 struct LinDecode {
     const void *q, *k, *v;

@@ -124,7 +124,7 @@ cudaError_t launch_run(LinRun r, int dx, int dz, bool chunk, bool bf16, const Se
 
 // Backward workspace regions.
 struct BwdLayout {
-    size_t dqf, dkf, dot_q, dot_k, snap_s, snap_g, partial, seg, total;
+    size_t dqf, dkf, snap_s, snap_g, partial, seg, total;
     int slots;
     Segments g;
 };
@@ -132,14 +132,12 @@ BwdLayout bwd_layout(const LinSizes &s, bool chunk)
 {
     BwdLayout L;
     L.g = segments(s, chunk);
-    L.slots = (int)(s.N + (s.rows + kda::LIN_SEG - 1) / kda::LIN_SEG);
-    const size_t grad = up256((size_t)s.rows * s.H * s.dk * 4), dots = up256((size_t)s.rows * s.H * 4);
+    L.slots = (int)(s.N + (s.rows + kda::SLOT_TOKENS - 1) / kda::SLOT_TOKENS);
+    const size_t grad = up256((size_t)s.rows * s.H * s.dk * 4);
     const size_t snap = up256((size_t)L.slots * s.H * s.dk * s.dv * 4);
     L.dqf = 0;
     L.dkf = L.dqf + grad;
-    L.dot_q = L.dkf + grad;
-    L.dot_k = L.dot_q + dots;
-    L.snap_s = L.dot_k + dots;
+    L.snap_s = L.dkf + grad;
     L.snap_g = L.snap_s + snap;
     L.partial = L.snap_g + snap;
     L.seg = L.partial + up256((size_t)L.slots * s.H * 4);
@@ -261,7 +259,7 @@ extern "C" int kda_linattn_chunk_bwd(int dtype, int B, int T, int Hk, int H, int
     r.s_in = initial_state;
     r.in_t = 1;
     r.snap = f32(L.snap_s);
-    r.snap_tokens = kda::LIN_SEG;
+    r.snap_tokens = kda::SLOT_TOKENS;
     r.out = f32(L.dqf);
     r.out_f32 = 1;
     cudaError_t e = launch_run(r, d_v, d_k, chunk, bf16, L.g, ws + L.seg, st);
@@ -274,7 +272,7 @@ extern "C" int kda_linattn_chunk_bwd(int dtype, int B, int T, int Hk, int H, int
     r.s_in = d_final_state;
     r.in_t = 1;
     r.snap = f32(L.snap_g);
-    r.snap_tokens = kda::LIN_SEG;
+    r.snap_tokens = kda::SLOT_TOKENS;
     r.out = f32(L.dkf);
     r.out_f32 = 1;
     if ((e = launch_run(r, d_v, d_k, chunk, bf16, L.g, ws + L.seg, st)) != cudaSuccess) return cuda_fail(e, "kda_linattn_chunk_bwd dk");
@@ -287,11 +285,11 @@ extern "C" int kda_linattn_chunk_bwd(int dtype, int B, int T, int Hk, int H, int
     r.s_out = d_initial_state;
     r.out = dv;
     if ((e = launch_run(r, d_k, d_v, chunk, bf16, L.g, ws + L.seg, st)) != cudaSuccess) return cuda_fail(e, "kda_linattn_chunk_bwd dv");
-    if ((e = kda::launch_lin_share(f32(L.dqf), f32(L.dkf), q, k, dq, dk, f32(L.dot_q), f32(L.dot_k), s.rows, Hk, H,
-                                   d_k, bf16, st)) != cudaSuccess)
+    if ((e = kda::launch_lin_share(f32(L.dqf), f32(L.dkf), dq, dk, s.rows, Hk, H, d_k, bf16, st)) != cudaSuccess)
         return cuda_fail(e, "kda_linattn_chunk_bwd head sums");
     kda::LinGateGrad gg{};
-    gg.dot_q = f32(L.dot_q); gg.dot_k = f32(L.dot_k);
+    gg.q = q; gg.k = k; gg.v = v; gg.d_o = d_o;
+    gg.s_init = initial_state;
     gg.snap_s = f32(L.snap_s); gg.snap_g = f32(L.snap_g);
     gg.g = g;
     gg.g_ld = g_per_token ? H : 0;
@@ -300,10 +298,10 @@ extern "C" int kda_linattn_chunk_bwd(int dtype, int B, int T, int Hk, int H, int
     gg.partial = g_per_token ? nullptr : f32(L.partial);
     gg.dg_head = g_per_token ? nullptr : dg;
     gg.rows = s.rows;
-    gg.H = H; gg.dk = d_k; gg.dv = d_v;
+    gg.Hk = Hk; gg.H = H; gg.dk = d_k; gg.dv = d_v;
     gg.num_seqs = s.N; gg.T = T; gg.slots = L.slots;
     gg.cu_seqlens = cu_seqlens;
-    if ((e = kda::launch_lin_gate_grad(gg, st)) != cudaSuccess) return cuda_fail(e, "kda_linattn_chunk_bwd dg");
+    if ((e = kda::launch_lin_gate_grad(gg, bf16, st)) != cudaSuccess) return cuda_fail(e, "kda_linattn_chunk_bwd dg");
     return KDA_OK;
 }
 
