@@ -62,16 +62,15 @@ struct LinGateGrad {
 cudaError_t launch_lin_scan(const LinRun &r, int dx, int dz, bool bf16, cudaStream_t st);
 // Chunks of a segment of the tensor-core form, 0 to leave sequences whole; and its slots
 // (segment j of sequence n is slot n + floor(R_n / tokens) + j, R_n its first row).
-int lin_segment_chunks(int num_seqs, int T, int H, long long rows, bool packed);
+int lin_segment_chunks(int num_seqs, int T, int H, int passes, long long rows, bool packed);
 inline int lin_segment_slots(int num_seqs, long long rows, int seg_chunks)
 {
     return (int)(num_seqs + (rows + seg_chunks * 64 - 1) / (seg_chunks * 64));
 }
 // Tensor-core form, bf16 only.
 bool lin_chunk_takes(int dx, int dz);
-cudaError_t launch_lin_states(const LinRun &r, int dx, int dz, cudaStream_t st);       // fills seg_state
-cudaError_t launch_lin_chunk(const LinRun &r, int dx, int dz, cudaStream_t st);        // bf16 outputs
-cudaError_t launch_lin_chunk_fine(const LinRun &r, int dx, int dz, cudaStream_t st);   // fp32 outputs
+// (1 to 3 passes of one shape, one cut of the token axis and one output type, side by side)
+cudaError_t launch_lin_chunk(const LinRun *r, int passes, int dx, int dz, cudaStream_t st);
 // Sums the per-value-head fp32 gradients over the heads that share a key head and casts them: dqf, dkf
 // [rows][H][dk]; dq, dk [rows][Hk][dk].
 cudaError_t launch_lin_share(const float *dqf, const float *dkf, void *dq, void *dk, long long rows, int Hk, int H,

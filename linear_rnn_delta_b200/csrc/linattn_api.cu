@@ -91,49 +91,56 @@ bool chunk_form(const LinSizes &s, unsigned flags)
 {
     return s.dtype == KDA_DTYPE_BF16 && !(flags & KDA_FLAG_FORCE_SCAN) && kda::lin_chunk_takes(s.dk, s.dv);
 }
-// Segments of the chunk form's token axis: their length and the workspace of their states and decays.
+// Segments of the chunk form's token axis: their length and the workspace of a pass's states and decays.
 struct Segments {
     int chunks, slots;
-    size_t states, totals, total;   // offsets and size in bytes
+    size_t totals, total;   // offset and size in bytes
 };
-Segments segments(const LinSizes &s, bool chunk)
+Segments segments(const LinSizes &s, int passes, bool chunk)
 {
     Segments g{};
-    if (chunk) g.chunks = kda::lin_segment_chunks(s.N, s.T, s.H, s.rows, s.packed);
+    if (chunk) g.chunks = kda::lin_segment_chunks(s.N, s.T, s.H, passes, s.rows, s.packed);
     if (!g.chunks) return g;
     g.slots = kda::lin_segment_slots(s.N, s.rows, g.chunks);
     g.totals = up256((size_t)g.slots * s.H * s.dk * s.dv * 4);
     g.total = g.totals + up256((size_t)g.slots * s.H * 4);
     return g;
 }
-// One pass; `seg_ws` holds the segments' workspace.
-cudaError_t launch_run(LinRun r, int dx, int dz, bool chunk, bool bf16, const Segments &g, uint8_t *seg_ws,
-                       cudaStream_t st)
+// Passes of one shape; `seg_ws` holds a segments' workspace for each.
+cudaError_t launch_runs(LinRun *r, int passes, int dx, int dz, bool chunk, bool bf16, const Segments &g, uint8_t *seg_ws,
+                        cudaStream_t st)
 {
-    if (!chunk) return kda::launch_lin_scan(r, dx, dz, bf16, st);
-    if (g.chunks) {
-        r.seg_chunks = g.chunks;
-        r.slots = g.slots;
-        r.seg_state = reinterpret_cast<float *>(seg_ws + g.states);
-        r.seg_total = reinterpret_cast<float *>(seg_ws + g.totals);
-        const cudaError_t e = kda::launch_lin_states(r, dx, dz, st);
-        if (e != cudaSuccess) return e;
+    if (!chunk) {
+        for (int i = 0; i < passes; ++i) {
+            const cudaError_t e = kda::launch_lin_scan(r[i], dx, dz, bf16, st);
+            if (e != cudaSuccess) return e;
+        }
+        return cudaSuccess;
     }
-    return r.out_f32 ? kda::launch_lin_chunk_fine(r, dx, dz, st) : kda::launch_lin_chunk(r, dx, dz, st);
+    for (int i = 0; g.chunks && i < passes; ++i) {
+        r[i].seg_chunks = g.chunks;
+        r[i].slots = g.slots;
+        r[i].seg_state = reinterpret_cast<float *>(seg_ws + i * g.total);
+        r[i].seg_total = reinterpret_cast<float *>(seg_ws + i * g.total + g.totals);
+    }
+    return kda::launch_lin_chunk(r, passes, dx, dz, st);
 }
 
 // Backward workspace regions.
 struct BwdLayout {
     size_t dqf, dkf, snap_s, snap_g, partial, seg, total;
-    int slots;
+    int slots, together;   // passes of one launch
     Segments g;
 };
 BwdLayout bwd_layout(const LinSizes &s, bool chunk)
 {
     BwdLayout L;
-    L.g = segments(s, chunk);
+    // dq, dk and dv are passes of one shape where d_k = d_v and their outputs have one type; dq and dk always are
+    const bool shared = s.H != s.Hk;
+    L.together = s.dk == s.dv && !shared ? 3 : 2;
+    L.g = segments(s, L.together, chunk);
     L.slots = (int)(s.N + (s.rows + kda::SLOT_TOKENS - 1) / kda::SLOT_TOKENS);
-    const size_t grad = up256((size_t)s.rows * s.H * s.dk * 4);
+    const size_t grad = shared ? up256((size_t)s.rows * s.H * s.dk * 4) : 0;   // of each value head
     const size_t snap = up256((size_t)L.slots * s.H * s.dk * s.dv * 4);
     L.dqf = 0;
     L.dkf = L.dqf + grad;
@@ -141,7 +148,7 @@ BwdLayout bwd_layout(const LinSizes &s, bool chunk)
     L.snap_g = L.snap_s + snap;
     L.partial = L.snap_g + snap;
     L.seg = L.partial + up256((size_t)L.slots * s.H * 4);
-    L.total = L.seg + L.g.total;
+    L.total = L.seg + L.together * L.g.total;
     return L;
 }
 
@@ -152,7 +159,7 @@ extern "C" size_t kda_linattn_chunk_fwd_workspace_size(int dtype, int B, int T, 
 {
     LinSizes s;
     if (lin_sizes(s, dtype, B, T, Hk, H, d_k, d_v, has_cu_seqlens != 0, num_seqs) != KDA_OK) return 0;
-    return segments(s, chunk_form(s, flags)).total;
+    return segments(s, 1, chunk_form(s, flags)).total;
 }
 
 extern "C" int kda_linattn_chunk_fwd(int dtype, int B, int T, int Hk, int H, int d_k, int d_v,
@@ -203,8 +210,8 @@ extern "C" int kda_linattn_chunk_fwd(int dtype, int B, int T, int Hk, int H, int
     r.snap_tokens = kda::SLOT_TOKENS;
     r.out = o;
     const bool chunk = chunk_form(s, flags);
-    const cudaError_t e = launch_run(r, d_k, d_v, chunk, dtype == KDA_DTYPE_BF16, segments(s, chunk),
-                                     static_cast<uint8_t *>(workspace), st);
+    const cudaError_t e = launch_runs(&r, 1, d_k, d_v, chunk, dtype == KDA_DTYPE_BF16, segments(s, 1, chunk),
+                                      static_cast<uint8_t *>(workspace), st);
     if (e != cudaSuccess) return cuda_fail(e, "kda_linattn_chunk_fwd launch");
     return KDA_OK;
 }
@@ -252,40 +259,40 @@ extern "C" int kda_linattn_chunk_bwd(int dtype, int B, int T, int Hk, int H, int
     const bool bf16 = dtype == KDA_DTYPE_BF16;
     const int group = H / Hk;
     auto f32 = [&](size_t off) { return reinterpret_cast<float *>(ws + off); };
+    LinRun runs[3];
     // dq_t = S_t do_t: forward in time, the state transposed
-    LinRun r = base_run(s, g, g_per_token, cu_seqlens);
-    r.x = d_o; r.y = v; r.z = k;
-    r.gz = group;
-    r.s_in = initial_state;
-    r.in_t = 1;
-    r.snap = f32(L.snap_s);
-    r.snap_tokens = kda::SLOT_TOKENS;
-    r.out = f32(L.dqf);
-    r.out_f32 = 1;
-    cudaError_t e = launch_run(r, d_v, d_k, chunk, bf16, L.g, ws + L.seg, st);
-    if (e != cudaSuccess) return cuda_fail(e, "kda_linattn_chunk_bwd dq");
+    LinRun &rq = runs[0] = base_run(s, g, g_per_token, cu_seqlens);
+    rq.x = d_o; rq.y = v; rq.z = k;
+    rq.gz = group;
+    rq.s_in = initial_state;
+    rq.in_t = 1;
+    rq.snap = f32(L.snap_s);
+    rq.snap_tokens = kda::SLOT_TOKENS;
+    rq.out = group > 1 ? f32(L.dqf) : dq;
+    rq.out_f32 = group > 1;
     // dk_t = G_t v_t: backward in time, the state transposed
-    r = base_run(s, g, g_per_token, cu_seqlens);
-    r.reverse = 1;
-    r.x = v; r.y = d_o; r.z = q;
-    r.gz = group;
-    r.s_in = d_final_state;
-    r.in_t = 1;
-    r.snap = f32(L.snap_g);
-    r.snap_tokens = kda::SLOT_TOKENS;
-    r.out = f32(L.dkf);
-    r.out_f32 = 1;
-    if ((e = launch_run(r, d_v, d_k, chunk, bf16, L.g, ws + L.seg, st)) != cudaSuccess) return cuda_fail(e, "kda_linattn_chunk_bwd dk");
+    LinRun &rk = runs[1] = base_run(s, g, g_per_token, cu_seqlens);
+    rk.reverse = 1;
+    rk.x = v; rk.y = d_o; rk.z = q;
+    rk.gz = group;
+    rk.s_in = d_final_state;
+    rk.in_t = 1;
+    rk.snap = f32(L.snap_g);
+    rk.snap_tokens = kda::SLOT_TOKENS;
+    rk.out = group > 1 ? f32(L.dkf) : dk;
+    rk.out_f32 = group > 1;
     // dv_t = G_t^T k_t: backward in time
-    r = base_run(s, g, g_per_token, cu_seqlens);
-    r.reverse = 1;
-    r.x = k; r.y = q; r.z = d_o;
-    r.gx = r.gy = group;
-    r.s_in = d_final_state;
-    r.s_out = d_initial_state;
-    r.out = dv;
-    if ((e = launch_run(r, d_k, d_v, chunk, bf16, L.g, ws + L.seg, st)) != cudaSuccess) return cuda_fail(e, "kda_linattn_chunk_bwd dv");
-    if ((e = kda::launch_lin_share(f32(L.dqf), f32(L.dkf), dq, dk, s.rows, Hk, H, d_k, bf16, st)) != cudaSuccess)
+    LinRun &rv = runs[2] = base_run(s, g, g_per_token, cu_seqlens);
+    rv.reverse = 1;
+    rv.x = k; rv.y = q; rv.z = d_o;
+    rv.gx = rv.gy = group;
+    rv.s_in = d_final_state;
+    rv.s_out = d_initial_state;
+    rv.out = dv;
+    cudaError_t e = launch_runs(runs, L.together, d_v, d_k, chunk, bf16, L.g, ws + L.seg, st);
+    if (e == cudaSuccess && L.together < 3) e = launch_runs(runs + 2, 1, d_k, d_v, chunk, bf16, L.g, ws + L.seg, st);
+    if (e != cudaSuccess) return cuda_fail(e, "kda_linattn_chunk_bwd passes");
+    if (group > 1 && (e = kda::launch_lin_share(f32(L.dqf), f32(L.dkf), dq, dk, s.rows, Hk, H, d_k, bf16, st)) != cudaSuccess)
         return cuda_fail(e, "kda_linattn_chunk_bwd head sums");
     kda::LinGateGrad gg{};
     gg.q = q; gg.k = k; gg.v = v; gg.d_o = d_o;

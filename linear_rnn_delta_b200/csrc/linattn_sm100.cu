@@ -86,14 +86,15 @@ static_assert(RG_P + 2 * RG_Z + RG_OUT + 2 * RG_STATE + RG_MMA <= 7 * 72, "more 
 // tensor-memory columns: KV, O, QK, the state's two parts, the scaled Z^T's three, Z^T
 constexpr uint32_t TM_KV = 0, TM_O = 128, TM_QK = 192, TM_S = 256, TM_ZP = 384, TM_Z = 480, TM_COLS = 512;
 
+// Up to three passes of one shape, blockIdx.y
 struct LinChunkParams {
-    LinRun a;
-    CUtensorMap tx, ty, tz, to;
+    LinRun a[3];
+    CUtensorMap x[3], y[3], z[3], o[3];
     unsigned *status;
 };
 
-// STATE: only the state that a segment adds from nothing, and its decay.
-template <int DX, int DZ, bool STATE>
+// STATE: only the state that a segment adds from nothing, and its decay.  OUT32: fp32 outputs.
+template <int DX, int DZ, bool STATE, bool OUT32>
 __global__ void __launch_bounds__(NT, 1) lin_chunk_kernel(const __grid_constant__ LinChunkParams P)
 {
     constexpr int JW = DZ / 32;                // warps with value channels of their own
@@ -104,7 +105,7 @@ __global__ void __launch_bounds__(NT, 1) lin_chunk_kernel(const __grid_constant_
     uint32_t *s_tmem = reinterpret_cast<uint32_t *>(sm + SM_MISC);
     volatile int *s_abort = reinterpret_cast<volatile int *>(sm + SM_MISC + 8);
     GateStage *gates = reinterpret_cast<GateStage *>(sm + SM_GATE);
-    const LinRun &a = P.a;
+    const LinRun &a = P.a[blockIdx.y];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, wg = warp >> 2;
     const int h = blockIdx.x % a.H;
     const bool rev = a.reverse != 0;
@@ -444,32 +445,44 @@ __global__ void __launch_bounds__(NT, 1) lin_chunk_kernel(const __grid_constant_
                             if (rev ? r + 1 <= from : r + 1 >= from) v[k].y = __int_as_float(0x7fc00000);
                         }
                     }
-                    uint32_t pk[8];
+                    if constexpr (OUT32) {   // a register's 32 values are 8 channels of 4 tokens: whole sectors
+                        float *o = (float *)a.out + ((size_t)row0 + t0) * ld + (size_t)h * DZ + q * 32 + g * 16 + (lane >> 2);
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) pk[k] = pack_bf16(v[k].x, v[k].y);
-                    // matrices: channels +0 / +8 of token group k, then of k + 1
-                    const uint32_t to = rows + half * 4096 + (((c0 + g * 2) ^ (r0 & 7)) << 4);
-                    stmatrix_x4_trans(to, pk[0], pk[1], pk[2], pk[3]);
-                    stmatrix_x4_trans(to + 2048, pk[4], pk[5], pk[6], pk[7]);
+                        for (int k = 0; k < 8; ++k) {
+                            const int r = half * 32 + (k >> 1) * 8 + 2 * (lane & 3);
+                            if (r < nv) o[r * ld + 8 * (k & 1)] = v[k].x;
+                            if (r + 1 < nv) o[(r + 1) * ld + 8 * (k & 1)] = v[k].y;
+                        }
+                    } else {
+                        uint32_t pk[8];
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) pk[k] = pack_bf16(v[k].x, v[k].y);
+                        // matrices: channels +0 / +8 of token group k, then of k + 1
+                        const uint32_t to = rows + half * 4096 + (((c0 + g * 2) ^ (r0 & 7)) << 4);
+                        stmatrix_x4_trans(to, pk[0], pk[1], pk[2], pk[3]);
+                        stmatrix_x4_trans(to + 2048, pk[4], pk[5], pk[6], pk[7]);
+                    }
                 }
             }
-            fence_async_smem();
-            group_sync(2, 128);
-            if (nv == C) {
-                if (tid == 3 * 128) {
+            if constexpr (!OUT32) {
+                fence_async_smem();
+                group_sync(2, 128);
+                if (nv == C) {
+                    if (tid == 3 * 128) {
 #pragma unroll
-                    for (int p = 0; p < DZ / 64; ++p)
-                        tma_store_3d(&P.to, sm + s * STAGE + p * 8192, p * 64, h, row0 + t0);
-                    bulk_commit();
-                    bulk_wait_read();
-                }
-            } else {
-                __nv_bfloat16 *o = (__nv_bfloat16 *)a.out + ((size_t)row0 + t0) * ld + (size_t)h * DZ;
+                        for (int p = 0; p < DZ / 64; ++p)
+                            tma_store_3d(&P.o[blockIdx.y], sm + s * STAGE + p * 8192, p * 64, h, row0 + t0);
+                        bulk_commit();
+                        bulk_wait_read();
+                    }
+                } else {
+                    __nv_bfloat16 *o = (__nv_bfloat16 *)a.out + ((size_t)row0 + t0) * ld + (size_t)h * DZ;
 #pragma unroll 1
-                for (int e = tid - 3 * 128; e < nv * (DZ / 8); e += 128) {
-                    const int r = e / (DZ / 8), ch = e % (DZ / 8);
-                    *reinterpret_cast<uint4 *>(o + r * ld + ch * 8) = *reinterpret_cast<const uint4 *>(
-                        sm + s * STAGE + (ch >> 3) * 8192 + r * 128 + (((ch & 7) ^ (r & 7)) << 4));
+                    for (int e = tid - 3 * 128; e < nv * (DZ / 8); e += 128) {
+                        const int r = e / (DZ / 8), ch = e % (DZ / 8);
+                        *reinterpret_cast<uint4 *>(o + r * ld + ch * 8) = *reinterpret_cast<const uint4 *>(
+                            sm + s * STAGE + (ch >> 3) * 8192 + r * 128 + (((ch & 7) ^ (r & 7)) << 4));
+                    }
                 }
             }
             warp_arrive(bar + B_EMPTY + s);
@@ -599,12 +612,12 @@ __global__ void __launch_bounds__(NT, 1) lin_chunk_kernel(const __grid_constant_
                     mbar_expect_tx(bar + B_FULL + s, ((STATE ? 1 : 2) * DX + DZ) * C * 2);
 #pragma unroll
                     for (int p = 0; p < DX / 64; ++p) {
-                        if (!STATE) tma_load_3d(st + p * 8192, &P.tx, bar + B_FULL + s, p * 64, hx, row0 + t0);
-                        tma_load_3d(st + TILE + p * 8192, &P.ty, bar + B_FULL + s, p * 64, hy, row0 + t0);
+                        if (!STATE) tma_load_3d(st + p * 8192, &P.x[blockIdx.y], bar + B_FULL + s, p * 64, hx, row0 + t0);
+                        tma_load_3d(st + TILE + p * 8192, &P.y[blockIdx.y], bar + B_FULL + s, p * 64, hy, row0 + t0);
                     }
 #pragma unroll
                     for (int p = 0; p < DZ / 64; ++p)
-                        tma_load_3d(st + 2 * TILE + p * 8192, &P.tz, bar + B_FULL + s, p * 64, hz, row0 + t0);
+                        tma_load_3d(st + 2 * TILE + p * 8192, &P.z[blockIdx.y], bar + B_FULL + s, p * 64, hz, row0 + t0);
                 }
             }
             // no load is in flight when the CTA ends, wound down early or not
@@ -705,58 +718,64 @@ __global__ void __launch_bounds__(256) lin_segment_kernel(const LinRun a, int dx
     if (nseg == 0 && a.s_out) *reinterpret_cast<float4 *>(a.s_out + (size_t)nh * size + e) = cur;
 }
 
-template <int DX, int DZ> cudaError_t make_params(LinChunkParams &p, const LinRun &r)
+template <int DX, int DZ> cudaError_t make_params(LinChunkParams &p, const LinRun *r, int passes)
 {
     memset(&p, 0, sizeof(p));
-    p.a = r;
-    const cudaError_t e = device_status_word(&p.status);
-    if (e != cudaSuccess) return e;
-    if (r.rows > 0 && (!make_map(&p.tx, r.x, r.rows, r.H / r.gx, DX) || !make_map(&p.ty, r.y, r.rows, r.H / r.gy, DX) ||
-                       !make_map(&p.tz, r.z, r.rows, r.H / r.gz, DZ) ||
-                       (!r.out_f32 && !make_map(&p.to, r.out, r.rows, r.H, DZ))))
-        return cudaErrorInvalidValue;
+    cudaError_t e = bind_context();
+    if (e != cudaSuccess || (e = device_status_word(&p.status)) != cudaSuccess) return e;
+    for (int i = 0; i < passes; ++i) {
+        p.a[i] = r[i];
+        if (r[i].rows > 0 && (!make_map(&p.x[i], r[i].x, r[i].rows, r[i].H / r[i].gx, DX) ||
+                              !make_map(&p.y[i], r[i].y, r[i].rows, r[i].H / r[i].gy, DX) ||
+                              !make_map(&p.z[i], r[i].z, r[i].rows, r[i].H / r[i].gz, DZ) ||
+                              (!r[i].out_f32 && !make_map(&p.o[i], r[i].out, r[i].rows, r[i].H, DZ))))
+            return cudaErrorInvalidValue;
+    }
     return cudaSuccess;
 }
 
-template <int DX, int DZ> cudaError_t launch_dims(const LinRun &r, cudaStream_t st)
+template <int DX, int DZ, bool STATE, bool OUT32>
+cudaError_t launch_kernel(const LinChunkParams &p, int passes, cudaStream_t st)
 {
     static bool done[64] = {};
-    cudaError_t e = opt_in(lin_chunk_kernel<DX, DZ, false>, SM_ALLOC, done);
+    const cudaError_t e = opt_in(lin_chunk_kernel<DX, DZ, STATE, OUT32>, SM_ALLOC, done);
     if (e != cudaSuccess) return e;
-    LinChunkParams p;
-    if ((e = make_params<DX, DZ>(p, r)) != cudaSuccess) return e;
+    const LinRun &r = p.a[0];
     const unsigned units = (unsigned)(r.seg_chunks ? r.slots : r.num_seqs);
-    lin_chunk_kernel<DX, DZ, false><<<units * r.H, NT, SM_ALLOC, st>>>(p);
+    lin_chunk_kernel<DX, DZ, STATE, OUT32><<<dim3(units * r.H, passes), NT, SM_ALLOC, st>>>(p);
     return cudaGetLastError();
 }
 
-template <int DX, int DZ> cudaError_t launch_states_dims(const LinRun &r, cudaStream_t st)
+template <int DX, int DZ> cudaError_t launch_dims(const LinRun *r, int passes, cudaStream_t st)
 {
-    static bool done[64] = {};
-    cudaError_t e = opt_in(lin_chunk_kernel<DX, DZ, true>, SM_ALLOC, done);
-    if (e != cudaSuccess) return e;
     LinChunkParams p;
-    if ((e = make_params<DX, DZ>(p, r)) != cudaSuccess) return e;
-    lin_chunk_kernel<DX, DZ, true><<<(unsigned)(r.slots * r.H), NT, SM_ALLOC, st>>>(p);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    lin_segment_kernel<<<dim3(r.num_seqs * r.H, (DX * DZ + 1023) / 1024), 256, 0, st>>>(r, DX, DZ);
-    return cudaGetLastError();
+    cudaError_t e = make_params<DX, DZ>(p, r, passes);
+    if (e != cudaSuccess) return e;
+    if (r->seg_chunks) {
+        if ((e = launch_kernel<DX, DZ, true, false>(p, passes, st)) != cudaSuccess) return e;
+        for (int i = 0; i < passes; ++i) {
+            lin_segment_kernel<<<dim3(r->num_seqs * r->H, (DX * DZ + 1023) / 1024), 256, 0, st>>>(r[i], DX, DZ);
+            if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        }
+    }
+    // passes of one launch have outputs of one type
+    return r->out_f32 ? launch_kernel<DX, DZ, false, true>(p, passes, st) : launch_kernel<DX, DZ, false, false>(p, passes, st);
 }
 
 }  // namespace
 
 bool lin_chunk_takes(int dx, int dz) { return (dx == 64 || dx == 128) && (dz == 64 || dz == 128); }
 
-int lin_segment_chunks(int num_seqs, int T, int H, long long rows, bool packed)
+int lin_segment_chunks(int num_seqs, int T, int H, int passes, long long rows, bool packed)
 {
     // Time in chunks of the kernel's walk.  Whole sequences: the waves of (sequence, head) pairs over the SMs, or
     // (packed, lengths unknown here) a longest sequence of three times the mean.  Cut: every chunk is walked twice, the
     // first time for its state alone (half a chunk's time), and a segment's start costs about 4 chunks.
     const int S = 148;
-    const double units = (double)num_seqs * H, all = (double)((rows + C - 1) / C) * H;
+    const double units = (double)num_seqs * H * passes, all = (double)((rows + C - 1) / C) * H * passes;
     const double mean = packed ? all / units : (double)((T + C - 1) / C);
     double whole = std::ceil(units / S) * mean;
-    if (packed) whole = std::max(whole, std::min(all / H, 3 * mean));
+    if (packed) whole = std::max(whole, std::min((double)((rows + C - 1) / C), 3 * mean));
     int best = 0;
     for (int waves = 1; waves <= 4; ++waves) {
         // packed: a sequence's last segment is half empty on average
@@ -773,21 +792,12 @@ int lin_segment_chunks(int num_seqs, int T, int H, long long rows, bool packed)
     return best;
 }
 
-cudaError_t launch_lin_states(const LinRun &r, int dx, int dz, cudaStream_t st)
+cudaError_t launch_lin_chunk(const LinRun *r, int passes, int dx, int dz, cudaStream_t st)
 {
-    if (dx == 128 && dz == 128) return launch_states_dims<128, 128>(r, st);
-    if (dx == 128 && dz == 64) return launch_states_dims<128, 64>(r, st);
-    if (dx == 64 && dz == 128) return launch_states_dims<64, 128>(r, st);
-    if (dx == 64 && dz == 64) return launch_states_dims<64, 64>(r, st);
-    return cudaErrorInvalidValue;
-}
-
-cudaError_t launch_lin_chunk(const LinRun &r, int dx, int dz, cudaStream_t st)
-{
-    if (dx == 128 && dz == 128) return launch_dims<128, 128>(r, st);
-    if (dx == 128 && dz == 64) return launch_dims<128, 64>(r, st);
-    if (dx == 64 && dz == 128) return launch_dims<64, 128>(r, st);
-    if (dx == 64 && dz == 64) return launch_dims<64, 64>(r, st);
+    if (dx == 128 && dz == 128) return launch_dims<128, 128>(r, passes, st);
+    if (dx == 128 && dz == 64) return launch_dims<128, 64>(r, passes, st);
+    if (dx == 64 && dz == 128) return launch_dims<64, 128>(r, passes, st);
+    if (dx == 64 && dz == 64) return launch_dims<64, 64>(r, passes, st);
     return cudaErrorInvalidValue;
 }
 

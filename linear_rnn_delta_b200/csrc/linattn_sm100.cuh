@@ -153,6 +153,15 @@ inline bool make_map(CUtensorMap *m, const void *base, long long rows, int heads
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Makes the current device's context the thread's own, which encoding a tensor map needs: a thread that has
+// made no runtime call yet (autograd's) has none.
+inline cudaError_t bind_context()
+{
+    int dev = 0;
+    const cudaError_t e = cudaGetDevice(&dev);
+    return e != cudaSuccess ? e : cudaSetDevice(dev);
+}
+
 // Per-device one-time set-up of a kernel: its dynamic shared memory.
 template <typename K> cudaError_t opt_in(K kernel, uint32_t bytes, bool (&done)[64])
 {
@@ -161,9 +170,6 @@ template <typename K> cudaError_t opt_in(K kernel, uint32_t bytes, bool (&done)[
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-    // makes the device's context the thread's current one, which encoding a tensor map needs: a thread
-    // that has made no runtime call yet (autograd's) has none
-    if ((e = cudaSetDevice(dev)) != cudaSuccess) return e;
     std::lock_guard<std::mutex> lock(mu);
     if (!done[dev]) {
         if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) != cudaSuccess) return e;

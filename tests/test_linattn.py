@@ -4,12 +4,13 @@ Tolerances.  A value that is a sum of products is compared with an allowance of 
 magnitudes, plus half a step of its output type relative to itself (bf16 2^-8, fp32 2^-24):
   - the token scan rounds the state twice a token and adds d products: c = (2 T + d + 8) 2^-24;
   - the chunked form splits fp32 factors into bf16 parts.  Two parts leave 2^-16 of the value at most (a rounding
-    is off by 2^-8 of the value, the second by 2^-8 of that): the state in o and dv.  The pairs' weights within a chunk are
-    rounded once in o and dv: 2^-8 of the sum over pairs of their magnitude, pair_size.  In a chunk that decays
-    by more than 2^-96 (`strong`) w_r x_r is rounded once instead, too: 2^-8 of A.  States, dq and dk have
-    three parts (2^-24) and keep the scan's allowance: their own additions are fewer than the scan's.
-dq, dk that several heads share are sums over them (A is, too).  Gate gradients are sums of q.dq - k.dk, whose
-sizes gate_sum_size adds up.
+    is off by 2^-8 of the value, the second by 2^-8 of that): the state in the outputs (o, dq, dk, dv).  The
+    pairs' weights within a chunk are rounded once there: 2^-8 of the sum over pairs of their magnitude, pair_size.
+    In a chunk that decays by more than 2^-96 (`strong`) the query side is rounded once instead, too: 2^-8 of A.
+    States have three parts (2^-24) and keep the scan's allowance: their own additions are fewer than the scan's.
+Gradients of shared heads are sums over them (A is, too).  Gate gradients sum the pairs' shares in fp32, each of them
+a product of sums over channels; gate_sum_size adds up their magnitudes (and those of the longer sums that they
+are a part of).
 """
 import math
 
@@ -70,7 +71,10 @@ def pairs(x, q, k, z, r, mag, strong, back=False):
     """Allowance for the weights that the chunked form rounds once."""
     if x["q"].dtype != torch.bfloat16:
         return 0.0
-    return 2.0 ** -8 * (ref.pair_size(q, k, z, r["g"], r["cu"], back) + (mag if strong else 0.0))
+    size = ref.pair_size(q, k, z, r["g"], r["cu"], back)
+    if mag.shape[2] != size.shape[2]:   # heads that share an output
+        size = size.unflatten(2, (mag.shape[2], -1)).sum(3)
+    return 2.0 ** -8 * (size + (mag if strong else 0.0))
 
 
 def check_fwd(kda, x, flags=0, states=False, strong=False):
@@ -111,8 +115,10 @@ def check_bwd(kda, x, flags=0, strong=False):
     size_g = ref.gate_sum_size(ab["q"], ab["k"], ab["g"], mag if r["g"].dim() > 1 else mag_tokens(mag, r), end, r["cu"])
     c, co = allowances(x["q"].dtype, T, dk, dv)
     step = STEP[x["q"].dtype]
-    near(got[0], want.dq, mag.dq, c, step, "dq")
-    near(got[1], want.dk, mag.dk, c, step, "dk")
+    group = r["v"].shape[2] // r["q"].shape[2]
+    qh, kh = (r[n].repeat_interleave(group, dim=2) for n in "qk")
+    near(got[0], want.dq, mag.dq + pairs(x, r["do"], r["v"], kh, r, mag.dq, strong) / co, co, step, "dq")
+    near(got[1], want.dk, mag.dk + pairs(x, r["do"], r["v"], qh, r, mag.dk, strong, back=True) / co, co, step, "dk")
     near(got[2], want.dv, mag.dv + pairs(x, r["q"], r["k"], r["do"], r, mag.dv, strong, back=True) / co, co, step, "dv")
     near(got[3], want.dg, size_g, c, STEP[torch.float32], "dg")
     near(got[4], want.ds0, mag.ds0, c, STEP[torch.float32], "d_initial_state")
