@@ -75,7 +75,9 @@ cudaError_t launch_lin_chunk(const LinRun *r, int passes, int dx, int dz, cudaSt
 // [rows][H][dk]; dq, dk [rows][Hk][dk].
 cudaError_t launch_lin_share(const float *dqf, const float *dkf, void *dq, void *dk, long long rows, int Hk, int H,
                              int d_k, bool bf16, cudaStream_t st);
-cudaError_t launch_lin_gate_grad(const LinGateGrad &a, bool bf16, cudaStream_t st);
+// `chunk`: the chunk form's kernel (bf16 inputs, head sizes that lin_chunk_takes)
+cudaError_t launch_lin_gate_grad(const LinGateGrad &a, bool bf16, bool chunk, cudaStream_t st);
+cudaError_t launch_lin_gate_chunk(const LinGateGrad &a, cudaStream_t st);
 
 struct LinDecode {
     const void *q, *k, *v;

@@ -308,7 +308,7 @@ extern "C" int kda_linattn_chunk_bwd(int dtype, int B, int T, int Hk, int H, int
     gg.Hk = Hk; gg.H = H; gg.dk = d_k; gg.dv = d_v;
     gg.num_seqs = s.N; gg.T = T; gg.slots = L.slots;
     gg.cu_seqlens = cu_seqlens;
-    if ((e = kda::launch_lin_gate_grad(gg, bf16, st)) != cudaSuccess) return cuda_fail(e, "kda_linattn_chunk_bwd dg");
+    if ((e = kda::launch_lin_gate_grad(gg, bf16, chunk, st)) != cudaSuccess) return cuda_fail(e, "kda_linattn_chunk_bwd dg");
     return KDA_OK;
 }
 

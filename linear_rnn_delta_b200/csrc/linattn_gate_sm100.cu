@@ -1,0 +1,317 @@
+// Gate gradient of linear attention's chunk form on the tensor cores: the sums of lin_gate_chunk_kernel
+// (linattn_grad.cu), for one chunk of 64 tokens and head,
+//   dg_t = sum_{s < t <= r} L_rs (q_r . k_s) (do_r . v_s) + sum_{r >= t} w_r do_r^T S_0 q_r
+//        + sum_{s < t} u_s v_s^T G_C k_s + e^{c_C} <S_0, G_C>,
+// S_0 and G_C as the dq and dk passes left them at the chunk's ends ([d_v][d_k], fp32).
+// Four products, D in tensor memory:  Q K^T and dO V^T (bf16 operands as loaded), and S_0 Q^T, G_C K^T
+// with lanes = value channels and the state in three bf16 parts (2^-24), A from tensor memory.  The rest
+// is fp32: the inner products over channels are lane sums, 32 tokens exchanged at once.
+// Bound by HBM: 2 states (8 d_k d_v bytes) and 4 tiles for each (chunk, head); two CTAs an SM cover each other's
+// latencies.
+#include "linattn_sm100.cuh"
+
+namespace kda {
+namespace {
+
+using namespace lin;
+
+constexpr int NT = 256;
+constexpr uint32_t SM_W = 4 * TILE;                      // q, k, dO, v tiles, then W [64][65]
+constexpr uint32_t SM_END = SM_W + 64 * 65 * 4;
+constexpr uint32_t SM_ALLOC = SM_END + 1024;
+constexpr uint32_t TM_D = 0, TM_S = 64, TM_COLS = 256;   // accumulator (the first product's second at TM_S), state parts
+
+struct GateParams {
+    LinGateGrad a;
+    CUtensorMap q, k, v, d_o;
+    unsigned *status;
+};
+
+template <int DK, int DV>
+__global__ void __launch_bounds__(NT, 2) lin_gate_kernel(const __grid_constant__ GateParams P)
+{
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    const uint32_t sb = smem_u32(sm);
+    float *s_w = reinterpret_cast<float *>(sm + SM_W);
+    __shared__ __align__(8) uint64_t s_bar[2];   // tiles; products
+    __shared__ uint32_t s_tmem;
+    __shared__ int s_abort;
+    __shared__ float2 s_c[C];
+    __shared__ float s_win[C], s_uout[C], s_red[2][4][C], s_dq[C], s_dk[C], s_x[NT / 32], s_tot, s_part[2];
+    const LinGateGrad &a = P.a;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, quarter = warp & 3, half = warp >> 2;
+    const int slot = blockIdx.x / a.H, h = blockIdx.x % a.H;
+    // sequence of the slot: the last one whose first slot is not behind it (first slots increase)
+    int n = 0;
+    {
+        int lo = 0, hi = a.num_seqs - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) / 2;
+            if (mid + (a.cu_seqlens ? a.cu_seqlens[mid] : mid * a.T) / C <= slot) lo = mid;
+            else hi = mid - 1;
+        }
+        n = lo;
+    }
+    const int row0 = a.cu_seqlens ? a.cu_seqlens[n] : n * a.T;
+    const int len = a.cu_seqlens ? a.cu_seqlens[n + 1] - row0 : a.T;
+    const int t0 = (slot - n - row0 / C) * C;
+    if (t0 < 0 || t0 >= len) {   // no chunk has this slot
+        if (a.partial && tid == 0) a.partial[(size_t)slot * a.H + h] = 0.f;
+        return;
+    }
+    const int nt = min(C, len - t0), hk = h / (a.H / a.Hk);
+    const size_t row = (size_t)row0 + t0;
+
+    if (warp == 0) tmem_alloc(&s_tmem, TM_COLS);
+    if (tid == 0) {
+        s_abort = 0;
+        mbar_init(s_bar, 1);
+        mbar_init(s_bar + 1, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        mbar_expect_tx(s_bar, (DK + DV) * 2 * C * 2);
+#pragma unroll
+        for (int p = 0; p < DK / 64; ++p) {
+            tma_load_3d(sm + p * 8192, &P.q, s_bar, p * 64, hk, (int)row);
+            tma_load_3d(sm + TILE + p * 8192, &P.k, s_bar, p * 64, hk, (int)row);
+        }
+#pragma unroll
+        for (int p = 0; p < DV / 64; ++p) {
+            tma_load_3d(sm + 2 * TILE + p * 8192, &P.d_o, s_bar, p * 64, h, (int)row);
+            tma_load_3d(sm + 3 * TILE + p * 8192, &P.v, s_bar, p * 64, h, (int)row);
+        }
+    }
+    if (warp == 1) {   // sums of log2-decays
+        const float g0 = 2 * lane < nt ? a.g[(row + 2 * lane) * a.g_ld + h] : 0.f;
+        const float g1 = 2 * lane + 1 < nt ? a.g[(row + 2 * lane + 1) * a.g_ld + h] : 0.f;
+        const bool nan = __any_sync(0xffffffffu, g0 != g0 || g1 != g1);
+        const long long f1 = fix_log2(fminf(fmaxf(g1, -1e4f), 1e4f));
+        long long run = fix_log2(fminf(fmaxf(g0, -1e4f), 1e4f)) + f1;
+        for (int off = 1; off < 32; off <<= 1) {
+            const long long o = __shfl_up_sync(0xffffffffu, run, off);
+            if (lane >= off) run += o;
+        }
+        const long long end = __shfl_sync(0xffffffffu, run, 31);
+        for (int e = 0; e < 2; ++e) {
+            const long long c = e ? run : run - f1;
+            const int t = 2 * lane + e;
+            s_c[t] = make_float2(nan ? NAN : (float)fix_int(c), fix_rest(c));
+            s_win[t] = nan ? NAN : fix_exp2(c);
+            s_uout[t] = nan ? NAN : fix_exp2(end - c);
+        }
+        if (lane == 0) s_tot = nan ? NAN : fix_exp2(end);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tbase = s_tmem, tlane = tbase + ((uint32_t)(quarter * 32) << 16);
+    bool ok = mbar_wait_cycles(s_bar, 0, WAIT_LIMIT);
+    ok = __syncthreads_and(ok) != 0;
+    uint32_t phase = 0;
+    // products are issued by warp 0, everybody waits for them
+    auto finish = [&]() {
+        if (warp == 0) mma_commit_warp(s_bar + 1, lane == 0);
+        ok = __syncthreads_and(mbar_wait_cycles(s_bar + 1, phase, WAIT_LIMIT)) != 0 && ok;
+        phase ^= 1;
+        tc_fence_after();
+    };
+
+    if (ok) {
+        // Q K^T and dO V^T; rows 64-127 of A are what lies behind: lanes nobody reads
+        constexpr uint32_t ID = idesc_bf16(128, C, false, false);
+        if (warp == 0) {
+            const uint32_t lead = lane == 0, q = k_tile(sb), k = k_tile(sb + TILE), d = k_tile(sb + 2 * TILE), v = k_tile(sb + 3 * TILE);
+#pragma unroll
+            for (int e = 0; e < DK / 16; ++e) mma_bf16_warp(tbase + TM_D, dK(q, e), dK(k, e), ID, e > 0, lead);
+#pragma unroll
+            for (int e = 0; e < DV / 16; ++e) mma_bf16_warp(tbase + TM_S, dK(d, e), dK(v, e), ID, e > 0, lead);
+        }
+        finish();
+        if (ok && quarter < 2) {   // row r of W, 32 columns
+            const int r = quarter * 32 + lane, s0 = half * 32;
+            float x[32], y[32];
+            tmem_ld32(tlane + TM_D + s0, x);
+            tmem_ld32(tlane + TM_S + s0, y);
+            tmem_wait_ld();
+            const float2 cr = s_c[r];
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+                s_w[r * 65 + s0 + e] = s0 + e < r ? x[e] * y[e] * ex2(diff(cr, s_c[s0 + e])) : 0.f;
+        }
+        tc_fence_before();
+        __syncthreads();
+        tc_fence_after();
+    }
+
+    // the two state products: S_0 with q, weighed by dO; G_C with k, weighed by v
+    const bool first = t0 == 0, last = t0 + nt >= len;
+    const size_t size = (size_t)DK * DV;
+    const float *st[2];
+    st[0] = first ? (a.s_init ? a.s_init + ((size_t)n * a.H + h) * size : nullptr)
+                  : a.snap_s + ((size_t)(slot - 1) * a.H + h) * size;
+    st[1] = last ? (a.g_end ? a.g_end + ((size_t)n * a.H + h) * size : nullptr)
+                 : a.snap_g + ((size_t)slot * a.H + h) * size;
+    const int j = quarter * 32 + lane, i0 = half * (DK / 2);
+    float accx = 0.f;
+#pragma unroll 1
+    for (int m = 0; m < 2; ++m) {
+        if (!ok || !st[m]) continue;   // (uniform)
+        if (j < DV) {
+            // the caller's states are [dk][dv], the passes' [dv][dk]
+            const bool t = m ? last : first;
+            const float *at = st[m] + (t ? (size_t)i0 * DV + j : (size_t)j * DK + i0);
+            const float *other = m == 0 && st[1] ? st[1] + (last ? (size_t)i0 * DV + j : (size_t)j * DK + i0) : nullptr;
+#pragma unroll 1
+            for (int b = 0; b < DK / 32; ++b) {   // 16 key channels
+                float x[16], z[16];
+                auto load = [&](float *to, const float *p, bool nat) {
+                    if (nat) {
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) to[e] = p[(size_t)(b * 16 + e) * DV];
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 16; e += 4)
+                            *reinterpret_cast<float4 *>(to + e) = *reinterpret_cast<const float4 *>(p + b * 16 + e);
+                    }
+                };
+                load(x, at, t);
+                if (other) {
+                    load(z, other, last);
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) accx = fmaf(x[e], z[e], accx);
+                }
+                uint32_t part[3][8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    float2 w = make_float2(x[2 * e], x[2 * e + 1]);
+                    part[0][e] = take_part(w);
+                    part[1][e] = take_part(w);
+                    part[2][e] = pack_bf16(w.x, w.y);
+                }
+#pragma unroll
+                for (int p = 0; p < 3; ++p) tmem_st8(tlane + TM_S + p * 64 + i0 / 2 + b * 8, part[p]);
+            }
+            tmem_wait_st();
+        }
+        tc_fence_before();
+        __syncthreads();
+        tc_fence_after();
+        if (warp == 0) {
+            constexpr uint32_t ID = idesc_bf16(128, C, false, false);
+            const uint32_t b = k_tile(sb + m * TILE);
+#pragma unroll 4
+            for (int e = 0; e < 3 * DK / 16; ++e) {
+                const int kk = e % (DK / 16);
+                mma_bf16_ts_warp(tbase + TM_D, tbase + TM_S + (e / (DK / 16)) * 64 + kk * 8, dK(b, kk), ID, e > 0, lane == 0);
+            }
+        }
+        finish();
+        if (ok) {
+            // this warp's 32 channels and 32 tokens: lane sums, halved and exchanged; lane l keeps token l
+            float y[32];
+            tmem_ld32(tlane + TM_D + half * 32, y);
+            tmem_wait_ld();
+            const uint8_t *tile = sm + (2 + m) * TILE + (j >> 6) * 8192;
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+                const int r = half * 32 + e;
+                const unsigned short w = *reinterpret_cast<const unsigned short *>(tile + r * 128 + (((j & 63) * 2) ^ ((r & 7) << 4)));
+                y[e] = j < DV ? y[e] * __uint_as_float((uint32_t)w << 16) : 0.f;
+            }
+#pragma unroll
+            for (int off = 16, cnt = 16; off; off >>= 1, cnt >>= 1) {
+                const bool up = (lane & off) != 0;
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    if (e < cnt) {
+                        const float send = up ? y[e] : y[e + cnt], keep = up ? y[e + cnt] : y[e];
+                        y[e] = keep + __shfl_xor_sync(0xffffffffu, send, off);
+                    }
+                }
+            }
+            s_red[m][quarter][half * 32 + lane] = y[0];
+        }
+        tc_fence_before();
+        __syncthreads();   // D and the parts are read
+        tc_fence_after();
+    }
+#pragma unroll
+    for (int off = 16; off; off >>= 1) accx += __shfl_xor_sync(0xffffffffu, accx, off);
+    if (lane == 0) s_x[warp] = accx;
+    __syncthreads();
+    if (tid < 2 * C) {
+        const int m = tid >> 6, r = tid & 63;
+        const float sum = st[m] ? (s_red[m][0][r] + s_red[m][1][r]) + (s_red[m][2][r] + s_red[m][3][r]) : 0.f;
+        if (m == 0) s_dq[r] = r < nt && st[0] ? s_win[r] * sum : 0.f;
+        else s_dk[r] = r < nt && st[1] ? s_uout[r] * sum : 0.f;
+    }
+    if (tid < C) {   // row prefixes of W: [r][t] = sum_{s < t} W_rs
+        float run = 0.f;
+        for (int s = 0; s < C; ++s) {
+            const float w = s_w[tid * 65 + s];
+            s_w[tid * 65 + s] = run;
+            run += w;
+        }
+    }
+    __syncthreads();
+    if (tid < C) {
+        const int t = tid;
+        float x = 0.f, y = 0.f, z = 0.f, cross = 0.f;
+        for (int r = nt - 1; r >= t; --r) {
+            x += s_w[r * 65 + t];
+            y += s_dq[r];
+        }
+        for (int s = 0; s < t; ++s) z += s_dk[s];
+        if (st[0] && st[1]) {
+            for (int w = 0; w < NT / 32; ++w) cross += s_x[w];
+            cross *= s_tot;
+        }
+        x = ok ? (x + y) + (z + cross) : NAN;
+        float sum = 0.f;
+        if (t < nt) {
+            // e^g has slope 0 at -infinity (the states' products may have an infinity's NaN there)
+            if (a.g[(row + t) * a.g_ld + h] == -INFINITY) x = 0.f;
+            if (a.dg) a.dg[(row + t) * a.H + h] = x;
+            sum = x;
+        }
+        if (a.partial) {
+#pragma unroll
+            for (int off = 16; off; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+            if (lane == 0) s_part[warp] = sum;
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (a.partial && tid == 0) a.partial[(size_t)slot * a.H + h] = s_part[0] + s_part[1];
+    if (!ok && tid == 0) atomicOr(P.status, DEV_WAIT_TIMEOUT);
+    if (warp == 0) tmem_dealloc(tbase, TM_COLS);
+}
+
+template <int DK, int DV> cudaError_t launch_dims(const LinGateGrad &a, cudaStream_t st)
+{
+    static bool done[64] = {};
+    cudaError_t e = opt_in(lin_gate_kernel<DK, DV>, SM_ALLOC, done);
+    GateParams p;
+    memset(&p, 0, sizeof(p));
+    p.a = a;
+    if (e != cudaSuccess || (e = bind_context()) != cudaSuccess || (e = device_status_word(&p.status)) != cudaSuccess) return e;
+    if (!make_map(&p.q, a.q, a.rows, a.Hk, DK) || !make_map(&p.k, a.k, a.rows, a.Hk, DK) ||
+        !make_map(&p.v, a.v, a.rows, a.H, DV) || !make_map(&p.d_o, a.d_o, a.rows, a.H, DV))
+        return cudaErrorInvalidValue;
+    lin_gate_kernel<DK, DV><<<(unsigned)((long long)a.slots * a.H), NT, SM_ALLOC, st>>>(p);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_lin_gate_chunk(const LinGateGrad &a, cudaStream_t st)
+{
+    if (a.dk == 128 && a.dv == 128) return launch_dims<128, 128>(a, st);
+    if (a.dk == 128 && a.dv == 64) return launch_dims<128, 64>(a, st);
+    if (a.dk == 64 && a.dv == 128) return launch_dims<64, 128>(a, st);
+    if (a.dk == 64 && a.dv == 64) return launch_dims<64, 64>(a, st);
+    return cudaErrorInvalidValue;
+}
+
+}  // namespace kda

@@ -314,11 +314,11 @@ template <typename TIn> cudaError_t launch_gate_dims(const LinGateGrad &a, cudaS
 
 }  // namespace
 
-cudaError_t launch_lin_gate_grad(const LinGateGrad &a, bool bf16, cudaStream_t st)
+cudaError_t launch_lin_gate_grad(const LinGateGrad &a, bool bf16, bool chunk, cudaStream_t st)
 {
     if ((long long)a.slots * a.H > 0x7fffffffll) return cudaErrorInvalidConfiguration;
     cudaError_t e = cudaSuccess;
-    if (a.rows > 0) e = bf16 ? launch_gate_dims<__nv_bfloat16>(a, st) : launch_gate_dims<float>(a, st);
+    if (a.rows > 0) e = chunk ? launch_lin_gate_chunk(a, st) : bf16 ? launch_gate_dims<__nv_bfloat16>(a, st) : launch_gate_dims<float>(a, st);
     if (e == cudaSuccess && a.dg_head) {
         lin_gate_head_kernel<<<a.H, 128, 0, st>>>(a.partial, a.rows > 0 ? a.slots : 0, a.H, a.dg_head);
         e = cudaGetLastError();
