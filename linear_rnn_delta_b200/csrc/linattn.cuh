@@ -32,7 +32,7 @@ struct LinRun {
     int num_seqs, T, H;
     const int32_t *cu_seqlens;  // packed batch, or NULL (sequence n is rows n*T .. n*T+T-1)
     long long rows;             // tokens of the whole batch
-    // tensor-core form, token axis in segments: chunks of one (0: not cut), slots of all sequences, and the state
+    // token axis in segments: chunks of 64 tokens of one (0: not cut), slots of all sequences, and the state
     // that enters each slot's segment [slot][H][d_x][d_z] with the decay over it [slot][H]
     int seg_chunks, slots;
     float *seg_state, *seg_total;
@@ -60,6 +60,9 @@ struct LinGateGrad {
 };
 
 cudaError_t launch_lin_scan(const LinRun &r, int dx, int dz, bool bf16, cudaStream_t st);
+int lin_scan_segment_chunks(int num_seqs, int H, int dx, int dz, long long rows);   // chunks of a segment, as below
+// Turns what each segment adds (seg_state, seg_total) into the states that enter them.
+cudaError_t launch_lin_segments(const LinRun &r, int dx, int dz, cudaStream_t st);
 // Chunks of a segment of the tensor-core form, 0 to leave sequences whole; and its slots
 // (segment j of sequence n is slot n + floor(R_n / tokens) + j, R_n its first row).
 int lin_segment_chunks(int num_seqs, int T, int H, int passes, long long rows, bool packed);

@@ -91,7 +91,7 @@ bool chunk_form(const LinSizes &s, unsigned flags)
 {
     return s.dtype == KDA_DTYPE_BF16 && !(flags & KDA_FLAG_FORCE_SCAN) && kda::lin_chunk_takes(s.dk, s.dv);
 }
-// Segments of the chunk form's token axis: their length and the workspace of a pass's states and decays.
+// Segments of the token axis: their length and the workspace of a pass's states and decays.
 struct Segments {
     int chunks, slots;
     size_t totals, total;   // offset and size in bytes
@@ -99,7 +99,8 @@ struct Segments {
 Segments segments(const LinSizes &s, int passes, bool chunk)
 {
     Segments g{};
-    if (chunk) g.chunks = kda::lin_segment_chunks(s.N, s.T, s.H, passes, s.rows, s.packed);
+    g.chunks = chunk ? kda::lin_segment_chunks(s.N, s.T, s.H, passes, s.rows, s.packed)
+                     : kda::lin_scan_segment_chunks(s.N, s.H, s.dk, s.dv, s.rows);
     if (!g.chunks) return g;
     g.slots = kda::lin_segment_slots(s.N, s.rows, g.chunks);
     g.totals = up256((size_t)g.slots * s.H * s.dk * s.dv * 4);
@@ -110,18 +111,18 @@ Segments segments(const LinSizes &s, int passes, bool chunk)
 cudaError_t launch_runs(LinRun *r, int passes, int dx, int dz, bool chunk, bool bf16, const Segments &g, uint8_t *seg_ws,
                         cudaStream_t st)
 {
+    for (int i = 0; g.chunks && i < passes; ++i) {
+        r[i].seg_chunks = g.chunks;
+        r[i].slots = g.slots;
+        r[i].seg_state = reinterpret_cast<float *>(seg_ws + i * g.total);
+        r[i].seg_total = reinterpret_cast<float *>(seg_ws + i * g.total + g.totals);
+    }
     if (!chunk) {
         for (int i = 0; i < passes; ++i) {
             const cudaError_t e = kda::launch_lin_scan(r[i], dx, dz, bf16, st);
             if (e != cudaSuccess) return e;
         }
         return cudaSuccess;
-    }
-    for (int i = 0; g.chunks && i < passes; ++i) {
-        r[i].seg_chunks = g.chunks;
-        r[i].slots = g.slots;
-        r[i].seg_state = reinterpret_cast<float *>(seg_ws + i * g.total);
-        r[i].seg_total = reinterpret_cast<float *>(seg_ws + i * g.total + g.totals);
     }
     return kda::launch_lin_chunk(r, passes, dx, dz, st);
 }
@@ -221,8 +222,9 @@ extern "C" size_t kda_linattn_chunk_bwd_workspace_size(int dtype, int B, int T, 
 {
     LinSizes s;
     if (lin_sizes(s, dtype, B, T, Hk, H, d_k, d_v, has_cu_seqlens != 0, num_seqs) != KDA_OK) return 0;
-    // the token scan (KDA_FLAG_FORCE_SCAN) needs no more than the chunk form
-    return bwd_layout(s, chunk_form(s, 0u)).total;
+    // with KDA_FLAG_FORCE_SCAN or without
+    const size_t scan = bwd_layout(s, false).total, chunk = bwd_layout(s, chunk_form(s, 0u)).total;
+    return scan > chunk ? scan : chunk;
 }
 
 extern "C" int kda_linattn_chunk_bwd(int dtype, int B, int T, int Hk, int H, int d_k, int d_v,

@@ -754,8 +754,7 @@ template <int DX, int DZ> cudaError_t launch_dims(const LinRun *r, int passes, c
     if (r->seg_chunks) {
         if ((e = launch_kernel<DX, DZ, true, false>(p, passes, st)) != cudaSuccess) return e;
         for (int i = 0; i < passes; ++i) {
-            lin_segment_kernel<<<dim3(r->num_seqs * r->H, (DX * DZ + 1023) / 1024), 256, 0, st>>>(r[i], DX, DZ);
-            if ((e = cudaGetLastError()) != cudaSuccess) return e;
+            if ((e = launch_lin_segments(r[i], DX, DZ, st)) != cudaSuccess) return e;
         }
     }
     // passes of one launch have outputs of one type
@@ -763,6 +762,12 @@ template <int DX, int DZ> cudaError_t launch_dims(const LinRun *r, int passes, c
 }
 
 }  // namespace
+
+cudaError_t launch_lin_segments(const LinRun &r, int dx, int dz, cudaStream_t st)
+{
+    lin_segment_kernel<<<dim3(r.num_seqs * r.H, (dx * dz + 1023) / 1024), 256, 0, st>>>(r, dx, dz);
+    return cudaGetLastError();
+}
 
 bool lin_chunk_takes(int dx, int dz) { return (dx == 64 || dx == 128) && (dz == 64 || dz == 128); }
 

@@ -5,7 +5,7 @@
 // scale for each (slot, head, key channel) costs 4 bytes in d_v.  With A = max |x| of the row and
 // TOP = 127 (int8) or 448 (e4m3):
 //   scale = A / TOP,   code = the code nearest to x TOP / A (ties to even),   value = code * scale.
-// The code is that of the exact quotient: x (TOP / A) in fp32 is off by at most 1.5 units in the last
+// The code is that of the exact quotient: x (TOP / A) in fp32 is off by a few units in the last
 // place, so only a quotient that close to a border between two codes can go to the wrong one, and
 // there the border times A is compared with x TOP in fp64, where both products are exact.
 //
@@ -25,41 +25,38 @@ constexpr unsigned DEV_BAD_INDEX = 4u;
 constexpr int SC_NT = 256;
 constexpr int SC_UNROLL = 4;
 
-// x TOP / A next to the border `m` (m > 0, |x| of it): -1, 0, 1 as the exact quotient lies below, on, above
+// |x| TOP / A against the border m > 0 between two codes: -1, 0, 1 as it lies below, on, above
 __device__ __noinline__ int border_side(float ax, float amax, float top, float m)
 {
     const double l = (double)ax * (double)top, r = (double)m * (double)amax;
     return l < r ? -1 : (l > r ? 1 : 0);
 }
-// |x| TOP / A as t (inv = TOP / A): int8 magnitude
-__device__ __forceinline__ float int8_mag(float ax, float amax, float inv)
+// Adding 1.5 * 2^23 rounds to a whole number (ties to even) and leaves it in the low bits, in two's complement:
+// the conversion instructions run at a quarter of this rate and bound the kernel (91 against 51 us of traffic).
+constexpr float MAGIC = 12582912.f;
+// x TOP / A (inv = TOP / A) as an int8 code in the low byte
+__device__ __forceinline__ uint32_t int8_code(float x, float amax, float inv)
 {
-    const float t = ax * inv;
-    float r = rintf(t);
-    const float f = floorf(t);
-    if (fabsf(t - f - 0.5f) < 6e-5f) {   // 127 * 1.5 units of 2^-23 is 2.3e-5
-        const int side = border_side(ax, amax, 127.f, f + 0.5f);
-        r = side < 0 ? f : (side > 0 ? f + 1.f : 2.f * rintf(0.5f * (f + 0.5f)));   // tie: the even neighbour
+    const float whole = fmaf(x, inv, MAGIC), r = whole - MAGIC, d = fmaf(x, inv, -r);
+    uint32_t code = __float_as_uint(whole);
+    if (fabsf(d) > 0.5f - 6e-5f) {   // inv is off by 2 units of 2^-23: 127 of those are 3e-5
+        const float m = fabsf(r + copysignf(0.5f, d));
+        const int side = border_side(fabsf(x), amax, 127.f, m);
+        const int below = (int)(m - 0.5f), mag = side < 0 ? below : side > 0 ? below + 1 : below + (below & 1);
+        code = (uint32_t)(x < 0.f ? -mag : mag);
     }
-    return r;
+    return code & 0xffu;
 }
 // e4m3: a value that rounds (to nearest even) to the exact quotient's code
 __device__ __forceinline__ float e4m3_mag(float ax, float amax, float inv)
 {
     float t = ax * inv;
-    float m;
-    bool near;
-    if (t >= 0.015625f) {   // normal codes: 3 stored bits, the border has the 20 below them at half
-        const uint32_t b = __float_as_uint(t);
-        const int d = (int)(b & 0xFFFFFu) - 0x80000;
-        near = d >= -4 && d <= 4;
-        m = __uint_as_float((b & ~0xFFFFFu) | 0x80000u);
-    } else {                // steps of 2^-9
-        const float u = t * 512.f, f = floorf(u) + 0.5f;
-        near = fabsf(u - f) < 8e-6f;
-        m = f * (1.f / 512.f);
-    }
-    if (near) {
+    const uint32_t b = __float_as_uint(t);
+    const float u = t * 512.f, r = (u + MAGIC) - MAGIC;
+    const bool normal = t >= 0.015625f;   // 3 stored bits, the border has the 20 below them at half; below: steps of 2^-9
+    const int d = (int)(b & 0xFFFFFu) - 0x80000;
+    if (normal ? d >= -8 && d <= 8 : fabsf(u - r) > 0.5f - 1.6e-5f) {   // t is off by 3 units at most
+        const float m = normal ? __uint_as_float((b & ~0xFFFFFu) | 0x80000u) : (r + copysignf(0.5f, u - r)) * (1.f / 512.f);
         const int side = border_side(ax, amax, 448.f, m);
         t = side == 0 ? m : __uint_as_float(__float_as_uint(m) + side);
     }
@@ -95,6 +92,7 @@ __global__ void __launch_bounds__(SC_NT) state_quantize_kernel(const StateCache 
     constexpr int PASS = SC_NT / 32 * RPW;        // rows of the CTA's pass
     for (int base = 0; base < a.dk; base += PASS * SC_UNROLL) {
         float4 x[SC_UNROLL];
+        uint32_t amax[SC_UNROLL];
 #pragma unroll
         for (int u = 0; u < SC_UNROLL; ++u) {
             const int k = base + u * PASS + warp * RPW + sub;
@@ -104,34 +102,26 @@ __global__ void __launch_bounds__(SC_NT) state_quantize_kernel(const StateCache 
         for (int u = 0; u < SC_UNROLL; ++u) {
             const int k = base + u * PASS + warp * RPW + sub;
             float v[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
-            float amax = 0.f;
-            bool bad = false;   // NaN or infinity: fmaxf would drop a NaN
+            // as integers, magnitudes order like the values, infinity and NaN above them
+            uint32_t most = 0;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                amax = fmaxf(amax, fabsf(v[e]));
-                bad |= !(fabsf(v[e]) <= 3.402823466e38f);
-            }
-            if (bad) amax = __int_as_float(0x7f800000);
+            for (int e = 0; e < 4; ++e) most = max(most, __float_as_uint(v[e]) & 0x7fffffffu);
 #pragma unroll
-            for (int off = LPR / 2; off; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
-            float scale = __fdiv_rn(amax, TOP);
-            const bool finite = amax <= 3.402823466e38f;
-            if (!finite) scale = __int_as_float(0x7fc00000);
+            for (int off = LPR / 2; off; off >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, off));
+            amax[u] = most;
             uint32_t word = 0;
-            if (finite && amax > 0.f) {
-                float am = amax;
-                if (amax < 1e-30f) {   // keep TOP / A in range: exact scaling of row and maximum
-                    am *= 18446744073709551616.f;
+            if (most < 0x7f800000u && most > 0u) {
+                float am = __uint_as_float(most);
+                if (am < 1e-30f || am > 1e30f) {   // keep the quotient's parts in range: exact scaling of row and maximum
+                    const float by = am < 1.f ? 18446744073709551616.f : 5.421010862427522e-20f;
+                    am *= by;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) v[e] *= 18446744073709551616.f;
+                    for (int e = 0; e < 4; ++e) v[e] *= by;
                 }
-                const float inv = __fdiv_rn(TOP, am);
+                const float inv = __fdividef(TOP, am);
                 if (FMT == FMT_INT8) {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int m = (int)int8_mag(fabsf(v[e]), am, inv);
-                        word |= (uint32_t)(uint8_t)(int8_t)(v[e] < 0.f ? -m : m) << (8 * e);
-                    }
+                    for (int e = 0; e < 4; ++e) word |= int8_code(v[e], am, inv) << (8 * e);
                 } else {
                     float t[4];
 #pragma unroll
@@ -140,11 +130,15 @@ __global__ void __launch_bounds__(SC_NT) state_quantize_kernel(const StateCache 
                            (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(t[2], t[3]), __NV_SATFINITE, __NV_E4M3) << 16;
                 }
             }
-            if (k < a.dk) {
-                dst[(size_t)k * LPR + c] = word;
-                if (c == 0) scales[k] = scale;
-            }
+            if (k < a.dk) dst[(size_t)k * LPR + c] = word;
         }
+        // a row's scale is one lane's: the u-th of its lanes has the u-th row's
+        uint32_t mine = amax[0];
+#pragma unroll
+        for (int u = 1; u < SC_UNROLL; ++u) mine = c == u ? amax[u] : mine;
+        const int k = base + c * PASS + warp * RPW + sub;
+        if (c < SC_UNROLL && k < a.dk)
+            scales[k] = mine < 0x7f800000u ? __fdiv_rn(__uint_as_float(mine), TOP) : __int_as_float(0x7fc00000);
     }
 }
 
