@@ -16,8 +16,9 @@ namespace {
 using namespace lin;
 
 constexpr int NT = 256;
-constexpr uint32_t SM_W = 4 * TILE;                      // q, k, dO, v tiles, then W [64][65]
-constexpr uint32_t SM_END = SM_W + 64 * 65 * 4;
+constexpr uint32_t SM_W = 4 * TILE;                      // q, k, dO, v tiles, then W [64][66]
+constexpr int WP = 66;                                   // W's row pitch
+constexpr uint32_t SM_END = SM_W + 64 * WP * 4;
 constexpr uint32_t SM_ALLOC = SM_END + 1024;
 constexpr uint32_t TM_D = 0, TM_S = 64, TM_COLS = 256;   // accumulator (the first product's second at TM_S), state parts
 
@@ -36,9 +37,8 @@ __global__ void __launch_bounds__(NT, 2) lin_gate_kernel(const __grid_constant__
     float *s_w = reinterpret_cast<float *>(sm + SM_W);
     __shared__ __align__(8) uint64_t s_bar[2];   // tiles; products
     __shared__ uint32_t s_tmem;
-    __shared__ int s_abort;
     __shared__ float2 s_c[C];
-    __shared__ float s_win[C], s_uout[C], s_red[2][4][C], s_dq[C], s_dk[C], s_x[NT / 32], s_tot, s_part[2];
+    __shared__ float s_win[C], s_uout[C], s_red[2][4][C], s_dq[C], s_dk[C], s_x[NT / 32], s_tot, s_pre[NT / 32][C];
     const LinGateGrad &a = P.a;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, quarter = warp & 3, half = warp >> 2;
     const int slot = blockIdx.x / a.H, h = blockIdx.x % a.H;
@@ -63,9 +63,21 @@ __global__ void __launch_bounds__(NT, 2) lin_gate_kernel(const __grid_constant__
     const int nt = min(C, len - t0), hk = h / (a.H / a.Hk);
     const size_t row = (size_t)row0 + t0;
 
+    // the states, on their way to L2 while the tiles are worked on
+    const bool first = t0 == 0, last = t0 + nt >= len;
+    const size_t size = (size_t)DK * DV;
+    const float *st[2];
+    st[0] = first ? (a.s_init ? a.s_init + ((size_t)n * a.H + h) * size : nullptr)
+                  : a.snap_s + ((size_t)(slot - 1) * a.H + h) * size;
+    st[1] = last ? (a.g_end ? a.g_end + ((size_t)n * a.H + h) * size : nullptr)
+                 : a.snap_g + ((size_t)slot * a.H + h) * size;
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+        if (st[m])
+            for (int e = tid; e < DK * DV / 32; e += NT) asm volatile("prefetch.global.L2 [%0];" :: "l"(st[m] + e * 32));
+
     if (warp == 0) tmem_alloc(&s_tmem, TM_COLS);
     if (tid == 0) {
-        s_abort = 0;
         mbar_init(s_bar, 1);
         mbar_init(s_bar + 1, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -136,7 +148,7 @@ __global__ void __launch_bounds__(NT, 2) lin_gate_kernel(const __grid_constant__
             const float2 cr = s_c[r];
 #pragma unroll
             for (int e = 0; e < 32; ++e)
-                s_w[r * 65 + s0 + e] = s0 + e < r ? x[e] * y[e] * ex2(diff(cr, s_c[s0 + e])) : 0.f;
+                s_w[r * WP + s0 + e] = s0 + e < r ? x[e] * y[e] * ex2(diff(cr, s_c[s0 + e])) : 0.f;
         }
         tc_fence_before();
         __syncthreads();
@@ -144,13 +156,6 @@ __global__ void __launch_bounds__(NT, 2) lin_gate_kernel(const __grid_constant__
     }
 
     // the two state products: S_0 with q, weighed by dO; G_C with k, weighed by v
-    const bool first = t0 == 0, last = t0 + nt >= len;
-    const size_t size = (size_t)DK * DV;
-    const float *st[2];
-    st[0] = first ? (a.s_init ? a.s_init + ((size_t)n * a.H + h) * size : nullptr)
-                  : a.snap_s + ((size_t)(slot - 1) * a.H + h) * size;
-    st[1] = last ? (a.g_end ? a.g_end + ((size_t)n * a.H + h) * size : nullptr)
-                 : a.snap_g + ((size_t)slot * a.H + h) * size;
     const int j = quarter * 32 + lane, i0 = half * (DK / 2);
     float accx = 0.f;
 #pragma unroll 1
@@ -245,45 +250,71 @@ __global__ void __launch_bounds__(NT, 2) lin_gate_kernel(const __grid_constant__
         if (m == 0) s_dq[r] = r < nt && st[0] ? s_win[r] * sum : 0.f;
         else s_dk[r] = r < nt && st[1] ? s_uout[r] * sum : 0.f;
     }
-    if (tid < C) {   // row prefixes of W: [r][t] = sum_{s < t} W_rs
-        float run = 0.f;
-        for (int s = 0; s < C; ++s) {
-            const float w = s_w[tid * 65 + s];
-            s_w[tid * 65 + s] = run;
-            run += w;
+    {   // p_r(t) = sum_{s < t} W_rs, summed over the warp's 8 rows r >= t; a lane has t = 2 lane, 2 lane + 1
+        float y0 = 0.f, y1 = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const int r = warp * 8 + e;
+            const float2 w = *reinterpret_cast<const float2 *>(s_w + r * WP + 2 * lane);
+            float run = w.x + w.y;
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const float o = __shfl_up_sync(0xffffffffu, run, off);
+                if (lane >= off) run += o;
+            }
+            float before = __shfl_up_sync(0xffffffffu, run, 1);
+            if (lane == 0) before = 0.f;
+            if (r >= 2 * lane && r < nt) y0 += before;
+            if (r >= 2 * lane + 1 && r < nt) y1 += before + w.x;
         }
+        s_pre[warp][2 * lane] = y0;
+        s_pre[warp][2 * lane + 1] = y1;
     }
     __syncthreads();
-    if (tid < C) {
-        const int t = tid;
-        float x = 0.f, y = 0.f, z = 0.f, cross = 0.f;
-        for (int r = nt - 1; r >= t; --r) {
-            x += s_w[r * 65 + t];
-            y += s_dq[r];
+    if (warp == 0) {   // t = 2 lane, 2 lane + 1
+        const int t = 2 * lane;
+        float x[2] = {0.f, 0.f};
+        for (int w = 0; w < NT / 32; ++w) {
+            x[0] += s_pre[w][t];
+            x[1] += s_pre[w][t + 1];
         }
-        for (int s = 0; s < t; ++s) z += s_dk[s];
+        const float q0 = s_dq[t], q1 = s_dq[t + 1], k0 = s_dk[t], k1 = s_dk[t + 1];
+        float after = q0 + q1, before = k0 + k1;   // sums of dq from t on, of dk up to t + 1
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const float o = __shfl_down_sync(0xffffffffu, after, off), u = __shfl_up_sync(0xffffffffu, before, off);
+            if (lane + off < 32) after += o;
+            if (lane >= off) before += u;
+        }
+        float sq = __shfl_down_sync(0xffffffffu, after, 1), sk = __shfl_up_sync(0xffffffffu, before, 1);
+        if (lane == 31) sq = 0.f;
+        if (lane == 0) sk = 0.f;
+        float cross = 0.f;
         if (st[0] && st[1]) {
             for (int w = 0; w < NT / 32; ++w) cross += s_x[w];
             cross *= s_tot;
         }
-        x = ok ? (x + y) + (z + cross) : NAN;
+        x[0] = (x[0] + (q0 + q1 + sq)) + (sk + cross);
+        x[1] = (x[1] + (q1 + sq)) + (sk + k0 + cross);
         float sum = 0.f;
-        if (t < nt) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            if (t + e >= nt) continue;
+            float d = ok ? x[e] : NAN;
             // e^g has slope 0 at -infinity (the states' products may have an infinity's NaN there)
-            if (a.g[(row + t) * a.g_ld + h] == -INFINITY) x = 0.f;
-            if (a.dg) a.dg[(row + t) * a.H + h] = x;
-            sum = x;
+            if (a.g[(row + t + e) * a.g_ld + h] == -INFINITY) d = 0.f;
+            if (a.dg) a.dg[(row + t + e) * a.H + h] = d;
+            sum += d;
         }
         if (a.partial) {
 #pragma unroll
             for (int off = 16; off; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-            if (lane == 0) s_part[warp] = sum;
+            if (lane == 0) a.partial[(size_t)slot * a.H + h] = sum;
         }
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (a.partial && tid == 0) a.partial[(size_t)slot * a.H + h] = s_part[0] + s_part[1];
     if (!ok && tid == 0) atomicOr(P.status, DEV_WAIT_TIMEOUT);
     if (warp == 0) tmem_dealloc(tbase, TM_COLS);
 }
