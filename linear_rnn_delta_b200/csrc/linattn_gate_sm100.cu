@@ -3,9 +3,9 @@
 //   dg_t = sum_{s < t <= r} L_rs (q_r . k_s) (do_r . v_s) + sum_{r >= t} w_r do_r^T S_0 q_r
 //        + sum_{s < t} u_s v_s^T G_C k_s + e^{c_C} <S_0, G_C>,
 // S_0 and G_C as the dq and dk passes left them at the chunk's ends ([d_v][d_k], fp32).
-// Four products, D in tensor memory:  Q K^T and dO V^T (bf16 operands as loaded), and S_0 Q^T, G_C K^T
-// with lanes = value channels and the state in three bf16 parts (2^-24), A from tensor memory.  The rest
-// is fp32: the inner products over channels are lane sums, 32 tokens exchanged at once.
+// Four products, D in tensor memory:  Q K^T and dO V^T (bf16 operands as loaded), and S_0 dO^T, G_C V^T
+// with lanes = key channels (in which the states are contiguous) and the state in three bf16 parts (2^-24), A from
+// tensor memory.  The rest is fp32: the inner products with q and k are lane sums, 32 tokens exchanged at once.
 // Bound by HBM: 2 states (8 d_k d_v bytes) and 4 tiles for each (chunk, head); two CTAs an SM cover each other's
 // latencies.
 #include "linattn_sm100.cuh"
@@ -66,15 +66,14 @@ __global__ void __launch_bounds__(NT, 2) lin_gate_kernel(const __grid_constant__
     // the states, on their way to L2 while the tiles are worked on
     const bool first = t0 == 0, last = t0 + nt >= len;
     const size_t size = (size_t)DK * DV;
-    const float *st[2];
-    st[0] = first ? (a.s_init ? a.s_init + ((size_t)n * a.H + h) * size : nullptr)
+    const float *st0 = first ? (a.s_init ? a.s_init + ((size_t)n * a.H + h) * size : nullptr)
                   : a.snap_s + ((size_t)(slot - 1) * a.H + h) * size;
-    st[1] = last ? (a.g_end ? a.g_end + ((size_t)n * a.H + h) * size : nullptr)
+    const float *st1 = last ? (a.g_end ? a.g_end + ((size_t)n * a.H + h) * size : nullptr)
                  : a.snap_g + ((size_t)slot * a.H + h) * size;
-#pragma unroll
-    for (int m = 0; m < 2; ++m)
-        if (st[m])
-            for (int e = tid; e < DK * DV / 32; e += NT) asm volatile("prefetch.global.L2 [%0];" :: "l"(st[m] + e * 32));
+    for (int e = tid; e < DK * DV / 32; e += NT) {
+        if (st0) asm volatile("prefetch.global.L2 [%0];" :: "l"(st0 + e * 32));
+        if (st1) asm volatile("prefetch.global.L2 [%0];" :: "l"(st1 + e * 32));
+    }
 
     if (warp == 0) tmem_alloc(&s_tmem, TM_COLS);
     if (tid == 0) {
@@ -155,33 +154,26 @@ __global__ void __launch_bounds__(NT, 2) lin_gate_kernel(const __grid_constant__
         tc_fence_after();
     }
 
-    // the two state products: S_0 with q, weighed by dO; G_C with k, weighed by v
-    const int j = quarter * 32 + lane, i0 = half * (DK / 2);
+    // the two state products: S_0 with dO, weighed by q; G_C with v, weighed by k
+    const int i = quarter * 32 + lane, j0 = half * (DV / 2);
     float accx = 0.f;
 #pragma unroll 1
     for (int m = 0; m < 2; ++m) {
-        if (!ok || !st[m]) continue;   // (uniform)
-        if (j < DV) {
+        if (!ok || !(m ? st1 : st0)) continue;   // (uniform)
+        if (i < DK) {
             // the caller's states are [dk][dv], the passes' [dv][dk]
-            const bool t = m ? last : first;
-            const float *at = st[m] + (t ? (size_t)i0 * DV + j : (size_t)j * DK + i0);
-            const float *other = m == 0 && st[1] ? st[1] + (last ? (size_t)i0 * DV + j : (size_t)j * DK + i0) : nullptr;
+            const bool nat = m ? last : first;
+            const float *at = (m ? st1 : st0) + (nat ? (size_t)i * DV + j0 : (size_t)j0 * DK + i);
+            const float *other = m == 0 && st1 ? st1 + (last ? (size_t)i * DV + j0 : (size_t)j0 * DK + i) : nullptr;
+            const int step = nat ? 1 : DK, ostep = last ? 1 : DK;
 #pragma unroll 1
-            for (int b = 0; b < DK / 32; ++b) {   // 16 key channels
+            for (int b = 0; b < DV / 32; ++b) {   // 16 value channels
                 float x[16], z[16];
-                auto load = [&](float *to, const float *p, bool nat) {
-                    if (nat) {
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) to[e] = p[(size_t)(b * 16 + e) * DV];
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 16; e += 4)
-                            *reinterpret_cast<float4 *>(to + e) = *reinterpret_cast<const float4 *>(p + b * 16 + e);
-                    }
-                };
-                load(x, at, t);
+                for (int e = 0; e < 16; ++e) x[e] = at[(b * 16 + e) * step];
                 if (other) {
-                    load(z, other, last);
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) z[e] = other[(b * 16 + e) * ostep];
 #pragma unroll
                     for (int e = 0; e < 16; ++e) accx = fmaf(x[e], z[e], accx);
                 }
@@ -194,7 +186,7 @@ __global__ void __launch_bounds__(NT, 2) lin_gate_kernel(const __grid_constant__
                     part[2][e] = pack_bf16(w.x, w.y);
                 }
 #pragma unroll
-                for (int p = 0; p < 3; ++p) tmem_st8(tlane + TM_S + p * 64 + i0 / 2 + b * 8, part[p]);
+                for (int p = 0; p < 3; ++p) tmem_st8(tlane + TM_S + p * 64 + j0 / 2 + b * 8, part[p]);
             }
             tmem_wait_st();
         }
@@ -203,11 +195,11 @@ __global__ void __launch_bounds__(NT, 2) lin_gate_kernel(const __grid_constant__
         tc_fence_after();
         if (warp == 0) {
             constexpr uint32_t ID = idesc_bf16(128, C, false, false);
-            const uint32_t b = k_tile(sb + m * TILE);
+            const uint32_t b = k_tile(sb + (2 + m) * TILE);
 #pragma unroll 4
-            for (int e = 0; e < 3 * DK / 16; ++e) {
-                const int kk = e % (DK / 16);
-                mma_bf16_ts_warp(tbase + TM_D, tbase + TM_S + (e / (DK / 16)) * 64 + kk * 8, dK(b, kk), ID, e > 0, lane == 0);
+            for (int e = 0; e < 3 * DV / 16; ++e) {
+                const int kk = e % (DV / 16);
+                mma_bf16_ts_warp(tbase + TM_D, tbase + TM_S + (e / (DV / 16)) * 64 + kk * 8, dK(b, kk), ID, e > 0, lane == 0);
             }
         }
         finish();
@@ -216,12 +208,12 @@ __global__ void __launch_bounds__(NT, 2) lin_gate_kernel(const __grid_constant__
             float y[32];
             tmem_ld32(tlane + TM_D + half * 32, y);
             tmem_wait_ld();
-            const uint8_t *tile = sm + (2 + m) * TILE + (j >> 6) * 8192;
+            const uint8_t *tile = sm + m * TILE + (i >> 6) * 8192;
 #pragma unroll
             for (int e = 0; e < 32; ++e) {
                 const int r = half * 32 + e;
-                const unsigned short w = *reinterpret_cast<const unsigned short *>(tile + r * 128 + (((j & 63) * 2) ^ ((r & 7) << 4)));
-                y[e] = j < DV ? y[e] * __uint_as_float((uint32_t)w << 16) : 0.f;
+                const unsigned short w = *reinterpret_cast<const unsigned short *>(tile + r * 128 + (((i & 63) * 2) ^ ((r & 7) << 4)));
+                y[e] = i < DK ? y[e] * __uint_as_float((uint32_t)w << 16) : 0.f;
             }
 #pragma unroll
             for (int off = 16, cnt = 16; off; off >>= 1, cnt >>= 1) {
@@ -246,9 +238,9 @@ __global__ void __launch_bounds__(NT, 2) lin_gate_kernel(const __grid_constant__
     __syncthreads();
     if (tid < 2 * C) {
         const int m = tid >> 6, r = tid & 63;
-        const float sum = st[m] ? (s_red[m][0][r] + s_red[m][1][r]) + (s_red[m][2][r] + s_red[m][3][r]) : 0.f;
-        if (m == 0) s_dq[r] = r < nt && st[0] ? s_win[r] * sum : 0.f;
-        else s_dk[r] = r < nt && st[1] ? s_uout[r] * sum : 0.f;
+        const float sum = (m ? st1 : st0) ? (s_red[m][0][r] + s_red[m][1][r]) + (s_red[m][2][r] + s_red[m][3][r]) : 0.f;
+        if (m == 0) s_dq[r] = r < nt && st0 ? s_win[r] * sum : 0.f;
+        else s_dk[r] = r < nt && st1 ? s_uout[r] * sum : 0.f;
     }
     {   // p_r(t) = sum_{s < t} W_rs, summed over the warp's 8 rows r >= t; a lane has t = 2 lane, 2 lane + 1
         float y0 = 0.f, y1 = 0.f;
@@ -290,7 +282,7 @@ __global__ void __launch_bounds__(NT, 2) lin_gate_kernel(const __grid_constant__
         if (lane == 31) sq = 0.f;
         if (lane == 0) sk = 0.f;
         float cross = 0.f;
-        if (st[0] && st[1]) {
+        if (st0 && st1) {
             for (int w = 0; w < NT / 32; ++w) cross += s_x[w];
             cross *= s_tot;
         }
