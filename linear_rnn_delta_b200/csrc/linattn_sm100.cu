@@ -33,8 +33,8 @@
 //   warps 12-15 outputs: w_r O -> bf16 -> [token][channel] tile -> TMA store
 //   warps 16-23 the state, fp32 in registers (a thread has half a row of R^T): R = e^{c_C} R + KV, split
 //   warp 24     loads (TMA, four stages of X, Y, Z)
-//   warp 25     issues KV_i and QK_{i+1}
-//   warp 26     issues O_i (one warp for all products spent longer on waits and issue than they take)
+//   warps 25-27 issue KV_i, O_i and QK_i (one warp for all products spent longer on waits and issue than they
+//               take, and QK waited behind KV)
 // Instruction fetch bounds such a kernel as soon as the roles' loops outgrow the SM's instruction cache:
 // loop bodies are kept short (rolled where registers allow), and waits sleep instead of polling.
 // Infinities and NaN: masked entries of P are selected, not multiplied, but 0 * NaN in Z^T P^T would
@@ -67,9 +67,9 @@ struct GateStage {
     short from[128];    // ... of channel j, first (backward: last) token
 };
 constexpr uint32_t SM_BAR = SM_GATE + NS * sizeof(GateStage);
-enum { B_FULL = 0, B_GATE = NS, B_EMPTY = 2 * NS, B_QKF = 3 * NS, B_QKE, B_PZ, B_OF = B_PZ + 2, B_KB = B_OF + 2,
-       B_KVF, B_S, B_SE, B_DRAIN, NBAR = B_DRAIN + 2 };
-// full: a stage's tiles; gate: its decays; empty: it may be loaded again; QKF, KVF, SE, OF: QK, KV, the state's product,
+enum { B_FULL = 0, B_EMPTY = NS, B_QKF = 2 * NS, B_QKE, B_PZ, B_OF = B_PZ + 2, B_KB = B_OF + 2,
+       B_KVF, B_S, B_SE, B_DRAIN, NBAR = B_DRAIN + 3 };
+// full: a stage's tiles and decays; empty: it may be loaded again; QKF, KVF, SE, OF: QK, KV, the state's product,
 // O are complete; QKE: QK is read; and what an MMA needs, all of it on one barrier (a wait costs the issuing
 // warp some 200 cycles even when it is over): PZ: P and Z^T for Z^T P^T; KB: Z^T's parts, and KV read, for KV;
 // S: the state's parts, and O read, for the state's product
@@ -120,8 +120,7 @@ __global__ void __launch_bounds__(NT, 1) lin_chunk_kernel(const __grid_constant_
     if (tid == 0) {
         *s_abort = 0;
         for (int s = 0; s < NS; ++s) {
-            mbar_init(bar + B_FULL + s, 1);
-            mbar_init(bar + B_GATE + s, 1);
+            mbar_init(bar + B_FULL + s, 2);   // the loads' bytes, the decays
             mbar_init(bar + B_EMPTY + s, STATE ? 1 + 2 * JW : 2 + 2 * JW + 4);   // products, state, outputs
         }
         mbar_init(bar + B_QKF, 1);
@@ -129,8 +128,8 @@ __global__ void __launch_bounds__(NT, 1) lin_chunk_kernel(const __grid_constant_
         for (int s = 0; s < 2; ++s) {
             mbar_init(bar + B_PZ + s, 2 + 8);
             mbar_init(bar + B_OF + s, 1);
-            mbar_init(bar + B_DRAIN + s, 1);
         }
+        for (int s = 0; s < 3; ++s) mbar_init(bar + B_DRAIN + s, 1);
         mbar_init(bar + B_KB, 8 + 2 * JW);
         mbar_init(bar + B_KVF, 1);
         mbar_init(bar + B_S, 2 * JW + JW);
@@ -154,7 +153,7 @@ __global__ void __launch_bounds__(NT, 1) lin_chunk_kernel(const __grid_constant_
                 const int s = i % NS, pb = i & 1;
                 const GateStage &G = gates[s];
                 // P's buffer is free once O_{i-2} has read it
-                if (!wait(bar + B_GATE + s, (i / NS) & 1, s_abort) || !wait(bar + B_QKF, i & 1, s_abort) ||
+                if (!wait(bar + B_FULL + s, (i / NS) & 1, s_abort) || !wait(bar + B_QKF, i & 1, s_abort) ||
                     (i >= 2 && !wait(bar + B_OF + pb, ((i >> 1) - 1) & 1, s_abort)))
                     break;
                 tc_fence_after();
@@ -274,7 +273,7 @@ __global__ void __launch_bounds__(NT, 1) lin_chunk_kernel(const __grid_constant_
                     G.nv = min(C, len - t0);
                     G.narrow = narrow;
                 }
-                warp_arrive(bar + B_GATE + s);
+                warp_arrive(bar + B_FULL + s);
             }
             if (STATE && lane == 0)
                 a.seg_total[(size_t)work.slot * a.H + h] = any_nan ? __int_as_float(0x7fc00000) : fix_exp2(sum);
@@ -294,9 +293,8 @@ __global__ void __launch_bounds__(NT, 1) lin_chunk_kernel(const __grid_constant_
             const int s = i % NS;
             GateStage &G = gates[s];
             uint8_t *st = sm + s * STAGE;
-            ok = ok && wait(bar + B_GATE + s, (i / NS) & 1, s_abort) && wait(bar + B_FULL + s, (i / NS) & 1, s_abort);
-            if (!group_sync_and(1, ZT, ok)) break;   // the group's barriers need all of it: it gives up together
-            const int nv = G.nv;
+            ok = ok && wait(bar + B_FULL + s, (i / NS) & 1, s_abort);
+            const int nv = min(C, len - chunk(i) * C);   // (not from G: barriers below depend on it, come what may)
             // rows of Y and Z behind the sequence's end belong to another one (or hold nothing): zero
             if (nv < C) {
                 const int p = (t & 31) >> 3;   // panel: Y's, then Z's
@@ -323,9 +321,11 @@ __global__ void __launch_bounds__(NT, 1) lin_chunk_kernel(const __grid_constant_
                     for (int e = 0; e < 8; ++e) most = max_abs2(most, max_abs2(z[0][e], z[1][e]));
                 }
                 if (pass) break;
-                clean = group_sync_and(1, ZT, (most & 0x7fffu) < 0x7f80u && (most & 0x7fff0000u) < 0x7f800000u);
+                clean = group_sync_and(1, ZT, ok && (most & 0x7fffu) < 0x7f80u && (most & 0x7fff0000u) < 0x7f800000u);
                 if (t == 0) G.bad = !clean;
                 if (clean) break;
+                ok = group_sync_and(1, ZT, ok);   // the group's barriers need all of it: it gives up together
+                if (!ok) break;
                 if (t < 128) {
                     int from = rev ? -1 : C;
                     if (t < DZ) {
@@ -344,7 +344,7 @@ __global__ void __launch_bounds__(NT, 1) lin_chunk_kernel(const __grid_constant_
                 }
                 group_sync(1, ZT);   // once more, without them
             }
-            if (i > 0) ok = wait(bar + B_KVF, (i - 1) & 1, s_abort);   // KV_{i-1} has read the parts
+            if (!ok) break;
             if (!STATE && !G.narrow) {   // w_r goes to X, which QK_i has read
                 ok = ok && wait(bar + B_QKF, i & 1, s_abort);
 #pragma unroll 1
@@ -359,12 +359,10 @@ __global__ void __launch_bounds__(NT, 1) lin_chunk_kernel(const __grid_constant_
                 }
                 fence_async_smem();
             }
-            if (!ok) continue;
-            if (q < JW) {
-                tc_fence_after();
+            uint32_t part[3][8];
 #pragma unroll 1
-                for (int g = 0; g < 2; ++g) {
-                    uint32_t part[3][8];
+            for (int g = 0; g < 2; ++g) {
+                if (q < JW) {
 #pragma unroll
                     for (int k = 0; k < 8; k += 2) {   // 8 tokens: u[k] channel lane/4, u[k+1] channel lane/4 + 8
                         const float2 u = *reinterpret_cast<const float2 *>(&G.u[part0 * 2 + 4 * k + 2 * (lane & 3)]);
@@ -376,13 +374,21 @@ __global__ void __launch_bounds__(NT, 1) lin_chunk_kernel(const __grid_constant_
                             part[2][k + e] = pack_bf16(x.x, x.y);
                         }
                     }
+                }
+                if (g == 0) {   // KV_{i-1} has read the parts
+                    if (i > 0) ok = ok && wait(bar + B_KVF, (i - 1) & 1, s_abort);
+                    if (!ok) break;
+                    tc_fence_after();
+                }
+                if (q < JW) {
 #pragma unroll
                     for (int p = 0; p < 3; ++p)
                         tmem_st_frag4(tlane + ((uint32_t)(g * 16) << 16) + TM_ZP + p * 32 + part0, part[p]);
                 }
-                tmem_wait_st();
-                tc_fence_before();
             }
+            if (!ok) continue;
+            tmem_wait_st();
+            tc_fence_before();
             warp_arrive(bar + B_KB);
             if (STATE) continue;
             // Z^T itself: O_{i-1} has read the last one
@@ -598,7 +604,7 @@ __global__ void __launch_bounds__(NT, 1) lin_chunk_kernel(const __grid_constant_
         }
     } else {
         regs_dec<RG_MMA>();
-        const uint32_t lead = lane == 0;
+        const uint32_t lead = elect_one();
         bool ok = true;
         if (warp == 24) {
             // ---- loads
@@ -624,32 +630,32 @@ __global__ void __launch_bounds__(NT, 1) lin_chunk_kernel(const __grid_constant_
             if (lane == 0)
                 for (int j = max(0, i - NS); j < i; ++j) mbar_wait_cycles(bar + B_FULL + j % NS, (j / NS) & 1, WAIT_LIMIT);
         } else if (warp == 25) {
-            // ---- KV_i and QK_{i+1}
-            constexpr uint32_t ID_QK = idesc_bf16(128, C, false, false), ID_KV = idesc_bf16(128, DX, false, true);
-            for (int i = -1; i < nch && ok; ++i) {
-                if (i >= 0) {
-                    ok = wait(bar + B_KB, i & 1, s_abort);
-                    if (!ok) break;
-                    tc_fence_after();
-                    const uint32_t y = mn_tile(sb + i % NS * STAGE + TILE);
+            // ---- KV_i
+            constexpr uint32_t ID_KV = idesc_bf16(128, DX, false, true);
+            for (int i = 0; i < nch; ++i) {
+                ok = wait(bar + B_KB, i & 1, s_abort);
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t y = mn_tile(sb + i % NS * STAGE + TILE);
 #pragma unroll 2
-                    for (int k = 0; k < 3 * C / 16; ++k)   // the parts' columns follow one another
-                        mma_bf16_ts_warp(tbase + TM_KV, tbase + TM_ZP + k * 8, dMN(y, k & (C / 16 - 1)), ID_KV, k > 0, lead);
-                    mma_commit_warp(bar + B_KVF, lead);
-                    mma_commit_warp(bar + B_EMPTY + i % NS, lead);
-                }
-                if (!STATE && i + 1 < nch) {   // rows 64-127 of A are what lies behind X: lanes nobody reads
-                    const int sn = (i + 1) % NS;
-                    const uint32_t x = k_tile(sb + sn * STAGE), y = k_tile(sb + sn * STAGE + TILE);
-                    ok = wait(bar + B_FULL + sn, ((i + 1) / NS) & 1, s_abort) &&
-                         (i < 0 || wait(bar + B_QKE, i & 1, s_abort));
-                    if (!ok) break;
-                    tc_fence_after();
+                for (int k = 0; k < 3 * C / 16; ++k)   // the parts' columns follow one another
+                    mma_bf16_ts_warp(tbase + TM_KV, tbase + TM_ZP + k * 8, dMN(y, k & (C / 16 - 1)), ID_KV, k > 0, lead);
+                mma_commit_warp(bar + B_KVF, lead);
+                mma_commit_warp(bar + B_EMPTY + i % NS, lead);
+            }
+        } else if (!STATE && warp == 27) {
+            // ---- QK_i; rows 64-127 of A are what lies behind X: lanes nobody reads
+            constexpr uint32_t ID_QK = idesc_bf16(128, C, false, false);
+            for (int i = 0; i < nch; ++i) {
+                const int s = i % NS;
+                ok = wait(bar + B_FULL + s, (i / NS) & 1, s_abort) && (i == 0 || wait(bar + B_QKE, (i - 1) & 1, s_abort));
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t x = k_tile(sb + s * STAGE), y = k_tile(sb + s * STAGE + TILE);
 #pragma unroll 2
-                    for (int k = 0; k < DX / 16; ++k)
-                        mma_bf16_warp(tbase + TM_QK, dK(x, k), dK(y, k), ID_QK, k > 0, lead);
-                    mma_commit_warp(bar + B_QKF, lead);
-                }
+                for (int k = 0; k < DX / 16; ++k)
+                    mma_bf16_warp(tbase + TM_QK, dK(x, k), dK(y, k), ID_QK, k > 0, lead);
+                mma_commit_warp(bar + B_QKF, lead);
             }
         } else if (!STATE && warp == 26) {
             // ---- O_i: the state's product and the chunk's
@@ -674,7 +680,7 @@ __global__ void __launch_bounds__(NT, 1) lin_chunk_kernel(const __grid_constant_
             }
         }
         // products still running are waited for here (every product of a full run is, by its readers)
-        if (!ok && (warp == 25 || warp == 26)) {
+        if (!ok && warp >= 25) {
             mma_commit_warp(bar + B_DRAIN + warp - 25, lead);
             if (lane == 0) mbar_wait_cycles(bar + B_DRAIN + warp - 25, 0, WAIT_LIMIT);
         }

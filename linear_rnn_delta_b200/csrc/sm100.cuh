@@ -117,6 +117,13 @@ __device__ __forceinline__ void mma_bf16_ts_warp(uint32_t d_tmem, uint32_t a_tme
         :: "r"(d_tmem), "r"(a_tmem), "r"(bdesc_lo), "r"(idesc), "r"(accumulate), "r"(leader), "n"(DESC_SW128_HI)
         : "memory");
 }
+// 1 in one lane of a converged warp, the same one each time
+__device__ __forceinline__ uint32_t elect_one()
+{
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(r));
+    return r;
+}
 __device__ __forceinline__ void mma_commit_warp(uint64_t *mbar, uint32_t leader)
 {
     asm volatile(
