@@ -692,6 +692,8 @@ __global__ void __launch_bounds__(NT, 1) lin_chunk_kernel(const __grid_constant_
     if (tid == 0 && *s_abort) atomicOr(P.status, DEV_WAIT_TIMEOUT);
 }
 
+constexpr int SEG_AHEAD = 8;
+
 // The states that enter the segments, in place of what each adds: one pass over a sequence's segments in time.
 // A thread has 4 values of one (sequence, head)'s state.
 __global__ void __launch_bounds__(256) lin_segment_kernel(const LinRun a, int dx, int dz)
@@ -711,14 +713,28 @@ __global__ void __launch_bounds__(256) lin_segment_kernel(const LinRun a, int dx
             cur = *reinterpret_cast<const float4 *>(s + e);
         }
     }
-    for (int t = 0; t < nseg; ++t) {
-        const size_t slot = (size_t)(first + (a.reverse ? nseg - 1 - t : t)) * a.H + h;
-        float4 *at = reinterpret_cast<float4 *>(a.seg_state + slot * size + e);
-        const float4 add = t + 1 < nseg ? *at : cur;
-        *at = cur;
-        if (t + 1 < nseg) {
-            const float d = a.seg_total[slot];
-            cur = make_float4(fmaf(d, cur.x, add.x), fmaf(d, cur.y, add.y), fmaf(d, cur.z, add.z), fmaf(d, cur.w, add.w));
+    // SEG_AHEAD segments' loads in flight: one by one their latencies add up (3 us a segment)
+    for (int t0 = 0; t0 < nseg; t0 += SEG_AHEAD) {
+        float4 *at[SEG_AHEAD], add[SEG_AHEAD];
+        float d[SEG_AHEAD];
+#pragma unroll
+        for (int b = 0; b < SEG_AHEAD; ++b) {
+            const int t = t0 + b;
+            if (t >= nseg) break;
+            const size_t slot = (size_t)(first + (a.reverse ? nseg - 1 - t : t)) * a.H + h;
+            at[b] = reinterpret_cast<float4 *>(a.seg_state + slot * size + e);
+            if (t + 1 < nseg) {   // (nothing was written for the last one)
+                add[b] = *at[b];
+                d[b] = a.seg_total[slot];
+            }
+        }
+#pragma unroll
+        for (int b = 0; b < SEG_AHEAD; ++b) {
+            if (t0 + b >= nseg) break;
+            *at[b] = cur;
+            if (t0 + b + 1 < nseg)
+                cur = make_float4(fmaf(d[b], cur.x, add[b].x), fmaf(d[b], cur.y, add[b].y),
+                                  fmaf(d[b], cur.z, add[b].z), fmaf(d[b], cur.w, add[b].w));
         }
     }
     if (nseg == 0 && a.s_out) *reinterpret_cast<float4 *>(a.s_out + (size_t)nh * size + e) = cur;
@@ -779,24 +795,30 @@ bool lin_chunk_takes(int dx, int dz) { return (dx == 64 || dx == 128) && (dz == 
 
 int lin_segment_chunks(int num_seqs, int T, int H, int passes, long long rows, bool packed)
 {
-    // Time in chunks of the kernel's walk.  Whole sequences: the waves of (sequence, head) pairs over the SMs, or
-    // (packed, lengths unknown here) a longest sequence of three times the mean.  Cut: every chunk is walked twice, the
-    // first time for its state alone (half a chunk's time), and a segment's start costs about 4 chunks.
+    // Time in chunks of the kernel's walk (1.85 us each at 128 x 128).  Whole: the waves of (sequence, head) pairs over
+    // the SMs, each of a sequence and a start (6 chunks).  Cut: every chunk is walked twice, the first time for
+    // its state alone, and each of a segment's two walks has a start (1.7 chunks a chunk and 16 a segment; 5 for the
+    // two further launches).
+    // Packed lengths, unknown here, are taken as exponential, cu_seqlens' rows divided by the sequences their mean:
+    // the longest of n has about mean (ln n + 0.58) chunks, and a sequence gives 1 / (1 - exp(-seg / mean)) segments.
+    // CTAs of unequal work fill the SMs but for half of the last one's.
+    // Measured, whole and cut as the rule takes them: 1x16x32768 953 and 241 us, 1x16x8192 248 and 84, 4x16x8192
+    // whole 250 (cut 261); 30 sequences of 65536 tokens, 4 heads, 232 and 173; 7 of 16384, 16 heads, whole 125 (cut 149).
     const int S = 148;
-    const double units = (double)num_seqs * H * passes, all = (double)((rows + C - 1) / C) * H * passes;
-    const double mean = packed ? all / units : (double)((T + C - 1) / C);
-    double whole = std::ceil(units / S) * mean;
-    if (packed) whole = std::max(whole, std::min((double)((rows + C - 1) / C), 3 * mean));
+    const double units = (double)num_seqs * H * passes;
+    const double mean = packed ? std::max(1.0, (double)rows / C / num_seqs) : (double)((T + C - 1) / C);
+    const double all = mean * units;
+    const double longest = mean * (packed ? std::max(1.0, std::log((double)num_seqs) + 0.58) : 1.0);
+    const double whole = packed ? std::max(longest + 6, (all + 6 * units) / S + 0.5 * longest)
+                                : std::ceil(units / S) * (mean + 6);
+    double least = 0.9 * whole;
     int best = 0;
-    for (int waves = 1; waves <= 4; ++waves) {
-        // packed: a sequence's last segment is half empty on average
-        const int seg = std::max(4, packed ? (int)std::ceil(all / (waves * (double)S))
-                                           : (int)std::ceil(mean / std::max(1.0, std::floor(waves * (double)S / units))));
-        if (seg >= mean * (packed ? 3 : 1)) continue;
-        const double count = packed ? units * 0.5 + all / seg : units * std::ceil(mean / seg);
-        const double cut = std::ceil(count / S) * (1.5 * seg + 4) + 4;
-        if (cut < 0.9 * whole) {
-            whole = cut / 0.9;
+    for (int seg = 4; seg < longest; seg += 1 + seg / 16) {
+        const double walk = 1.7 * seg + 16;
+        const double cut = packed ? std::max(walk, (1.7 * all + 16 * units / (1 - std::exp(-seg / mean))) / S + 0.5 * walk) + 5
+                                  : std::ceil(units * std::ceil(mean / seg) / S) * walk + 5;
+        if (cut < least) {
+            least = cut;
             best = seg;
         }
     }

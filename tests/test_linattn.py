@@ -427,6 +427,85 @@ def test_validation_flag(kda):
         assert e.value.code == 1
 
 
+CUT = [  # few long sequences, walked in segments side by side: dtype, B, T, Hk, H, dk, dv, cu, init, per_head
+    ("bf16", 1, 2177, 1, 2, 64, 64, None, True, False),
+    ("bf16", 1, 2048, 1, 1, 128, 128, None, False, False),
+    ("bf16", 1, 2049, 1, 1, 64, 128, None, True, True),
+    ("bf16", 2, 2111, 1, 1, 128, 64, None, True, False),
+    ("bf16", 1, 4500, 1, 2, 64, 64, [0, 3, 3, 2100, 4500], True, False),
+    ("bf16", 1, 4500, 1, 1, 64, 64, [0, 4436, 4436, 4500], False, False),
+    ("bf16", 1, 2177, 1, 1, 32, 64, None, True, False),
+    ("fp32", 1, 2177, 1, 2, 64, 64, None, True, False),
+    ("fp32", 1, 2500, 2, 2, 16, 32, [0, 1, 1, 1217, 1281, 2500], True, True),
+]
+
+
+def assert_cut(kda, c):
+    dt, B, T, Hk, H, dk, dv, cu = c[:8]
+    sizes = (0 if dt == "bf16" else 1, B, T, Hk, H, dk, dv, int(cu is not None), B if cu is None else len(cu) - 1, 0)
+    assert kda.lib.kda_linattn_chunk_fwd_workspace_size(*sizes) > 0   # the segments' states
+
+
+@pytest.mark.parametrize("c", CUT, ids=str)
+def test_the_long_cases_are_cut(kda, c):
+    assert_cut(kda, c)
+
+
+@gpu
+@pytest.mark.parametrize("c", CUT, ids=str)
+def test_cut_sequences(kda, c):
+    check_fwd(kda, make(21, *((DT[c[0]],) + c[1:]), rate=0.3), states=True)
+    check_bwd(kda, make(22, *((DT[c[0]],) + c[1:]), rate=0.3))
+
+
+@gpu
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_resets_in_cut_sequences(kda, dtype):
+    """Resets at, before and behind the segments' borders (multiples of 64 here), and a whole segment of them."""
+    x = make(23, DT[dtype], 1, 2200, 1, 1, 64, 64, init=True, rate=0.2)
+    x["g"][0, [63, 64, 255, 256, 257, 1023, 1024, 2047, 2048, 2199]] = -math.inf
+    x["g"][0, 512:900] = -math.inf
+    x["g"][0, 1200:1500] = 0.0
+    x["g"][0, 1600:1700] = -20.0
+    check_fwd(kda, x, states=True, strong=True)
+    check_bwd(kda, x, strong=True)
+
+
+@gpu
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_cut_sequences_keep_what_is_behind_apart(kda, dtype):
+    """NaN in a token leaves what is before it and the other sequences as they are; the final state may be the
+    initial one; two streams and a replayed graph give the same bits."""
+    x = make(24, DT[dtype], 1, 4500, 1, 2, 64, 64, cu=[0, 3, 2100, 4500], init=True, rate=0.2)
+    d = dev(x)
+    run = lambda y, **kw: kda.kda_linattn_chunk_fwd(  # noqa: E731
+        y["q"], y["k"], y["v"], y["g"], cu_seqlens=y["cu"], **kw)
+    want, sf = run(d, initial_state=d["s0"])
+    for name in "kv":
+        y = dev(x)
+        y[name][0, 1500] = math.nan
+        o, s = run(y, initial_state=y["s0"])
+        for part in (slice(0, 1500), slice(2100, 4500)):
+            assert torch.equal(o[0, part], want[0, part]), name
+        assert torch.isnan(o[0, 1500:2100].float()).all() and torch.isnan(s[1]).all()
+        assert torch.equal(s[0], sf[0]) and torch.equal(s[2], sf[2])
+    state = d["s0"].clone()
+    o, s = run(d, initial_state=state, final_state=state)
+    assert s is state and torch.equal(o, want) and torch.equal(s, sf)
+    torch.cuda.synchronize()
+    outs = [run(d, initial_state=d["s0"], stream=st) for st in [torch.cuda.Stream() for _ in range(3)] for _ in range(2)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, want) and torch.equal(b, sf) for a, b in outs)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        o, s = run(d, initial_state=d["s0"])
+    for _ in range(2):
+        o.zero_(), s.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(o, want) and torch.equal(s, sf)
+
+
 # ---- refusals (CPU) ------------------------------------------------------------------------------------------------
 
 def test_binding_refuses(kda):
