@@ -36,6 +36,9 @@ struct LinRun {
     // that enters each slot's segment [slot][H][d_x][d_z] with the decay over it [slot][H]
     int seg_chunks, slots;
     float *seg_state, *seg_total;
+    // segments in turn (tensor-core form): tickets given out [H] and state hand-overs done [slot][H], zero at the
+    // launch; NULL: side by side
+    int *tickets, *handed;
 };
 
 __device__ __forceinline__ int lin_row0(const LinRun &a, int n) { return a.cu_seqlens ? a.cu_seqlens[n] : n * a.T; }
@@ -63,9 +66,14 @@ cudaError_t launch_lin_scan(const LinRun &r, int dx, int dz, bool bf16, cudaStre
 int lin_scan_segment_chunks(int num_seqs, int H, int dx, int dz, long long rows);   // chunks of a segment, as below
 // Turns what each segment adds (seg_state, seg_total) into the states that enter them.
 cudaError_t launch_lin_segments(const LinRun &r, int dx, int dz, cudaStream_t st);
-// Chunks of a segment of the tensor-core form, 0 to leave sequences whole; and its slots
-// (segment j of sequence n is slot n + floor(R_n / tokens) + j, R_n its first row).
-int lin_segment_chunks(int num_seqs, int T, int H, int passes, long long rows, bool packed);
+// The tensor-core form's cut: chunks of a segment (0: sequences are left whole), and whether a sequence's segments
+// are walked in turn; and the segments' slots (segment j of sequence n is slot n + floor(R_n / tokens) + j, R_n its
+// first row).
+struct LinCut {
+    int chunks;
+    bool turns;
+};
+LinCut lin_cut(int num_seqs, int T, int H, int passes, long long rows, bool packed);
 inline int lin_segment_slots(int num_seqs, long long rows, int seg_chunks)
 {
     return (int)(num_seqs + (rows + seg_chunks * 64 - 1) / (seg_chunks * 64));

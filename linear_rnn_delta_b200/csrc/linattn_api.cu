@@ -94,17 +94,27 @@ bool chunk_form(const LinSizes &s, unsigned flags)
 // Segments of the token axis: their length and the workspace of a pass's states and decays.
 struct Segments {
     int chunks, slots;
-    size_t totals, total;   // offset and size in bytes
+    bool turns;
+    size_t sync;            // bytes of all passes' tickets and hand-overs, first in the workspace
+    size_t totals, total;   // a pass's offset and size in bytes
+    size_t bytes;
 };
 Segments segments(const LinSizes &s, int passes, bool chunk)
 {
     Segments g{};
-    g.chunks = chunk ? kda::lin_segment_chunks(s.N, s.T, s.H, passes, s.rows, s.packed)
-                     : kda::lin_scan_segment_chunks(s.N, s.H, s.dk, s.dv, s.rows);
+    if (chunk) {
+        const kda::LinCut cut = kda::lin_cut(s.N, s.T, s.H, passes, s.rows, s.packed);
+        g.chunks = cut.chunks;
+        g.turns = cut.turns;
+    } else {
+        g.chunks = kda::lin_scan_segment_chunks(s.N, s.H, s.dk, s.dv, s.rows);
+    }
     if (!g.chunks) return g;
     g.slots = kda::lin_segment_slots(s.N, s.rows, g.chunks);
+    g.sync = g.turns ? up256((size_t)passes * (1 + g.slots) * s.H * 4) : 0;
     g.totals = up256((size_t)g.slots * s.H * s.dk * s.dv * 4);
-    g.total = g.totals + up256((size_t)g.slots * s.H * 4);
+    g.total = g.totals + (g.turns ? 0 : up256((size_t)g.slots * s.H * 4));
+    g.bytes = g.sync + passes * g.total;
     return g;
 }
 // Passes of one shape; `seg_ws` holds a segments' workspace for each.
@@ -114,8 +124,17 @@ cudaError_t launch_runs(LinRun *r, int passes, int dx, int dz, bool chunk, bool 
     for (int i = 0; g.chunks && i < passes; ++i) {
         r[i].seg_chunks = g.chunks;
         r[i].slots = g.slots;
-        r[i].seg_state = reinterpret_cast<float *>(seg_ws + i * g.total);
-        r[i].seg_total = reinterpret_cast<float *>(seg_ws + i * g.total + g.totals);
+        r[i].seg_state = reinterpret_cast<float *>(seg_ws + g.sync + i * g.total);
+        if (g.turns) {
+            r[i].tickets = reinterpret_cast<int *>(seg_ws) + (size_t)i * (1 + g.slots) * r[i].H;
+            r[i].handed = r[i].tickets + r[i].H;
+        } else {
+            r[i].seg_total = reinterpret_cast<float *>(seg_ws + g.sync + i * g.total + g.totals);
+        }
+    }
+    if (g.turns) {
+        const cudaError_t e = cudaMemsetAsync(seg_ws, 0, g.sync, st);
+        if (e != cudaSuccess) return e;
     }
     if (!chunk) {
         for (int i = 0; i < passes; ++i) {
@@ -149,7 +168,7 @@ BwdLayout bwd_layout(const LinSizes &s, bool chunk)
     L.snap_g = L.snap_s + snap;
     L.partial = L.snap_g + snap;
     L.seg = L.partial + up256((size_t)L.slots * s.H * 4);
-    L.total = L.seg + L.together * L.g.total;
+    L.total = L.seg + L.g.bytes;
     return L;
 }
 
@@ -160,7 +179,7 @@ extern "C" size_t kda_linattn_chunk_fwd_workspace_size(int dtype, int B, int T, 
 {
     LinSizes s;
     if (lin_sizes(s, dtype, B, T, Hk, H, d_k, d_v, has_cu_seqlens != 0, num_seqs) != KDA_OK) return 0;
-    return segments(s, 1, chunk_form(s, flags)).total;
+    return segments(s, 1, chunk_form(s, flags)).bytes;
 }
 
 extern "C" int kda_linattn_chunk_fwd(int dtype, int B, int T, int Hk, int H, int d_k, int d_v,

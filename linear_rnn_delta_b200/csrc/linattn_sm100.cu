@@ -86,8 +86,34 @@ static_assert(RG_P + 2 * RG_Z + RG_OUT + 2 * RG_STATE + RG_MMA <= 7 * 72, "more 
 // tensor-memory columns: KV, O, QK, the state's two parts, the scaled Z^T's three, Z^T
 constexpr uint32_t TM_KV = 0, TM_O = 128, TM_QK = 192, TM_S = 256, TM_ZP = 384, TM_Z = 480, TM_COLS = 512;
 
-// Up to three passes of one shape, blockIdx.y
+// A state between the CTAs of two segments: each warp that wrote its part counts it, and all are waited for.
+__device__ __forceinline__ void hand_over(int *count)
+{
+    asm volatile("red.release.gpu.global.add.s32 [%0], 1;" ::"l"(count) : "memory");
+}
+__device__ __forceinline__ bool wait_handed(const int *count, int all, volatile int *abort)
+{
+    bool ok = true;
+    if ((threadIdx.x & 31) == 0) {
+        const long long t0 = clock64();
+        for (;;) {
+            int v;
+            asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(count) : "memory");
+            if (v >= all) break;
+            if (*abort || clock64() - t0 > WAIT_LIMIT) {
+                *abort = 1;
+                ok = false;
+                break;
+            }
+            __nanosleep(200);
+        }
+    }
+    return __all_sync(0xffffffffu, ok);
+}
+
+// Up to three passes of one shape; CTAs of a unit's passes and heads are neighbours
 struct LinChunkParams {
+    int passes;
     LinRun a[3];
     CUtensorMap x[3], y[3], z[3], o[3];
     unsigned *status;
@@ -105,14 +131,17 @@ __global__ void __launch_bounds__(NT, 1) lin_chunk_kernel(const __grid_constant_
     uint32_t *s_tmem = reinterpret_cast<uint32_t *>(sm + SM_MISC);
     volatile int *s_abort = reinterpret_cast<volatile int *>(sm + SM_MISC + 8);
     GateStage *gates = reinterpret_cast<GateStage *>(sm + SM_GATE);
-    const LinRun &a = P.a[blockIdx.y];
+    const int h = blockIdx.x % P.a[0].H, pass = blockIdx.x / P.a[0].H % P.passes;
+    const LinRun &a = P.a[pass];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, wg = warp >> 2;
-    const int h = blockIdx.x % a.H;
     const bool rev = a.reverse != 0;
-    const Work work = lin_work(a, blockIdx.x / a.H);
+    const bool turns = !STATE && a.tickets;
+    const Work work = turns ? lin_turn(a, h, reinterpret_cast<int *>(sm + SM_GATE)) : lin_work(a, blockIdx.x / a.H / P.passes);
     const int n = work.n, row0 = work.row0, len = work.len, nch = work.nch;
-    if (a.seg_chunks && nch <= 0) return;
-    const bool closing = rev ? work.c0 == 0 : work.c0 + nch == work.nall;   // the sequence's last segment in time
+    if (turns ? work.slot < 0 : a.seg_chunks && nch <= 0) return;
+    // the sequence's first and last segment in time
+    const bool opening = rev ? work.c0 + nch >= work.nall : work.c0 == 0;
+    const bool closing = rev ? work.c0 == 0 : work.c0 + nch >= work.nall;
     if (STATE && closing) return;   // nobody asks for the state behind it
     const size_t soff = ((size_t)n * a.H + h) * DX * DZ, woff = ((size_t)work.slot * a.H + h) * DX * DZ;
 
@@ -477,7 +506,7 @@ __global__ void __launch_bounds__(NT, 1) lin_chunk_kernel(const __grid_constant_
                     if (tid == 3 * 128) {
 #pragma unroll
                         for (int p = 0; p < DZ / 64; ++p)
-                            tma_store_3d(&P.o[blockIdx.y], sm + s * STAGE + p * 8192, p * 64, h, row0 + t0);
+                            tma_store_3d(&P.o[pass], sm + s * STAGE + p * 8192, p * 64, h, row0 + t0);
                         bulk_commit();
                         bulk_wait_read();
                     }
@@ -501,19 +530,25 @@ __global__ void __launch_bounds__(NT, 1) lin_chunk_kernel(const __grid_constant_
         constexpr int CX = DX / 2;
         if ((warp & 3) < JW) {
             const int j = (warp & 3) * 32 + lane, i0 = (wg - 4) * CX;
-            const float *s_in = STATE ? nullptr : a.seg_chunks ? a.seg_state + woff : a.s_in ? a.s_in + soff : nullptr;
-            float *s_out = STATE ? a.seg_state + woff : a.s_out && closing ? a.s_out + soff : nullptr;
+            const bool given = !STATE && a.seg_chunks && !(turns && opening);   // by other segments' walks
+            const float *s_in = STATE ? nullptr : given ? a.seg_state + woff : a.s_in ? a.s_in + soff : nullptr;
+            const bool gives = turns && !closing;   // in turn: to the slot behind this one in time
+            const size_t to_slot = (size_t)(work.slot + (rev ? -1 : 1)) * a.H + h;
+            float *s_out = STATE ? a.seg_state + woff : gives ? a.seg_state + to_slot * (DX * DZ)
+                           : a.s_out && closing ? a.s_out + soff : nullptr;
+            bool ok = true;
+            if (turns && given) ok = wait_handed(a.handed + (size_t)work.slot * a.H + h, 2 * JW, s_abort);
             // between memory and the registers by way of the tensor memory that KV has later: short loops
             const uint32_t scratch = tlane + TM_KV + i0;
             {
-                const bool t = s_in && a.in_t && !a.seg_chunks;
+                const bool t = s_in && a.in_t && !given;
                 const float *at = s_in + (t ? (size_t)j * DX + i0 : (size_t)i0 * DZ + j);
                 const int step = t ? 1 : DZ;
 #pragma unroll 1
                 for (int b = 0; b < CX / 16; ++b, at += 16 * step) {
                     float v[16];
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) v[e] = s_in ? at[e * step] : 0.f;
+                    for (int e = 0; e < 16; ++e) v[e] = s_in ? __ldcg(at + e * step) : 0.f;
                     tmem_st16(scratch + b * 16, v);
                 }
                 tmem_wait_st();
@@ -522,9 +557,8 @@ __global__ void __launch_bounds__(NT, 1) lin_chunk_kernel(const __grid_constant_
 #pragma unroll
             for (int b = 0; b < CX / 16; ++b) tmem_ld16(scratch + b * 16, &S[b * 8].x);
             tmem_wait_ld();
-            bool ok = true;
             // iteration i: the state before it is published (and written where it is a boundary's or the last)
-            for (int i = 0;; ++i) {
+            for (int i = 0; ok; ++i) {
                 if ((!STATE && a.snap) || i == nch) {
                     float *to[2] = {nullptr, nullptr};
                     // the token whose boundary this state is: backward the chunk to come ends there, forward the
@@ -601,6 +635,10 @@ __global__ void __launch_bounds__(NT, 1) lin_chunk_kernel(const __grid_constant_
             if (!ok && s_out)
 #pragma unroll 1
                 for (int e = 0; e < CX; ++e) s_out[(size_t)(i0 + e) * DZ + j] = __int_as_float(0x7fc00000);
+            if (gives) {
+                __syncwarp();
+                if (lane == 0) hand_over(a.handed + to_slot);
+            }
         }
     } else {
         regs_dec<RG_MMA>();
@@ -618,12 +656,12 @@ __global__ void __launch_bounds__(NT, 1) lin_chunk_kernel(const __grid_constant_
                     mbar_expect_tx(bar + B_FULL + s, ((STATE ? 1 : 2) * DX + DZ) * C * 2);
 #pragma unroll
                     for (int p = 0; p < DX / 64; ++p) {
-                        if (!STATE) tma_load_3d(st + p * 8192, &P.x[blockIdx.y], bar + B_FULL + s, p * 64, hx, row0 + t0);
-                        tma_load_3d(st + TILE + p * 8192, &P.y[blockIdx.y], bar + B_FULL + s, p * 64, hy, row0 + t0);
+                        if (!STATE) tma_load_3d(st + p * 8192, &P.x[pass], bar + B_FULL + s, p * 64, hx, row0 + t0);
+                        tma_load_3d(st + TILE + p * 8192, &P.y[pass], bar + B_FULL + s, p * 64, hy, row0 + t0);
                     }
 #pragma unroll
                     for (int p = 0; p < DZ / 64; ++p)
-                        tma_load_3d(st + 2 * TILE + p * 8192, &P.z[blockIdx.y], bar + B_FULL + s, p * 64, hz, row0 + t0);
+                        tma_load_3d(st + 2 * TILE + p * 8192, &P.z[pass], bar + B_FULL + s, p * 64, hz, row0 + t0);
                 }
             }
             // no load is in flight when the CTA ends, wound down early or not
@@ -743,6 +781,7 @@ __global__ void __launch_bounds__(256) lin_segment_kernel(const LinRun a, int dx
 template <int DX, int DZ> cudaError_t make_params(LinChunkParams &p, const LinRun *r, int passes)
 {
     memset(&p, 0, sizeof(p));
+    p.passes = passes;
     cudaError_t e = bind_context();
     if (e != cudaSuccess || (e = device_status_word(&p.status)) != cudaSuccess) return e;
     for (int i = 0; i < passes; ++i) {
@@ -757,14 +796,14 @@ template <int DX, int DZ> cudaError_t make_params(LinChunkParams &p, const LinRu
 }
 
 template <int DX, int DZ, bool STATE, bool OUT32>
-cudaError_t launch_kernel(const LinChunkParams &p, int passes, cudaStream_t st)
+cudaError_t launch_kernel(const LinChunkParams &p, cudaStream_t st)
 {
     static bool done[64] = {};
     const cudaError_t e = opt_in(lin_chunk_kernel<DX, DZ, STATE, OUT32>, SM_ALLOC, done);
     if (e != cudaSuccess) return e;
     const LinRun &r = p.a[0];
     const unsigned units = (unsigned)(r.seg_chunks ? r.slots : r.num_seqs);
-    lin_chunk_kernel<DX, DZ, STATE, OUT32><<<dim3(units * r.H, passes), NT, SM_ALLOC, st>>>(p);
+    lin_chunk_kernel<DX, DZ, STATE, OUT32><<<units * r.H * p.passes, NT, SM_ALLOC, st>>>(p);
     return cudaGetLastError();
 }
 
@@ -773,14 +812,14 @@ template <int DX, int DZ> cudaError_t launch_dims(const LinRun *r, int passes, c
     LinChunkParams p;
     cudaError_t e = make_params<DX, DZ>(p, r, passes);
     if (e != cudaSuccess) return e;
-    if (r->seg_chunks) {
-        if ((e = launch_kernel<DX, DZ, true, false>(p, passes, st)) != cudaSuccess) return e;
+    if (r->seg_chunks && !r->tickets) {
+        if ((e = launch_kernel<DX, DZ, true, false>(p, st)) != cudaSuccess) return e;
         for (int i = 0; i < passes; ++i) {
             if ((e = launch_lin_segments(r[i], DX, DZ, st)) != cudaSuccess) return e;
         }
     }
     // passes of one launch have outputs of one type
-    return r->out_f32 ? launch_kernel<DX, DZ, false, true>(p, passes, st) : launch_kernel<DX, DZ, false, false>(p, passes, st);
+    return r->out_f32 ? launch_kernel<DX, DZ, false, true>(p, st) : launch_kernel<DX, DZ, false, false>(p, st);
 }
 
 }  // namespace
@@ -793,17 +832,19 @@ cudaError_t launch_lin_segments(const LinRun &r, int dx, int dz, cudaStream_t st
 
 bool lin_chunk_takes(int dx, int dz) { return (dx == 64 || dx == 128) && (dz == 64 || dz == 128); }
 
-int lin_segment_chunks(int num_seqs, int T, int H, int passes, long long rows, bool packed)
+LinCut lin_cut(int num_seqs, int T, int H, int passes, long long rows, bool packed)
 {
     // Time in chunks of the kernel's walk (1.85 us each at 128 x 128).  Whole: the waves of (sequence, head) pairs over
-    // the SMs, each of a sequence and a start (6 chunks).  Cut: every chunk is walked twice, the first time for
-    // its state alone, and each of a segment's two walks has a start (1.7 chunks a chunk and 16 a segment; 5 for the
-    // two further launches).
+    // the SMs, each of a sequence and a start (6 chunks).  Cut, side by side: every chunk is walked twice, the first
+    // time for its state alone, and each of a segment's two walks has a start (1.7 chunks a chunk and 16 a segment; 5
+    // for the two further launches).  Cut, in turn: each is walked once, but a sequence's one after the other.
     // Packed lengths, unknown here, are taken as exponential, cu_seqlens' rows divided by the sequences their mean:
     // the longest of n has about mean (ln n + 0.58) chunks, and a sequence gives 1 / (1 - exp(-seg / mean)) segments.
     // CTAs of unequal work fill the SMs but for half of the last one's.
-    // Measured, whole and cut as the rule takes them: 1x16x32768 953 and 241 us, 1x16x8192 248 and 84, 4x16x8192
-    // whole 250 (cut 261); 30 sequences of 65536 tokens, 4 heads, 232 and 173; 7 of 16384, 16 heads, whole 125 (cut 149).
+    // Measured, whole and as taken, 16 heads of 128 x 128: 1x32768 953 and 241 us, 1x8192 248 and 84, 4x8192 whole 250
+    // (side by side 261), 12x4096 283 and 222 (in turn), 10x8192 543 and 386 (in turn), backward of 4x4096 670 and 595
+    // (in turn); packed, 30 sequences of 65536 tokens, 4 heads, 246 and 186 (side by side); 7 of 16384 whole 129
+    // (in turn 140); 16 of 32768, 32 heads, 427 and 359 (in turn).
     const int S = 148;
     const double units = (double)num_seqs * H * passes;
     const double mean = packed ? std::max(1.0, (double)rows / C / num_seqs) : (double)((T + C - 1) / C);
@@ -812,14 +853,19 @@ int lin_segment_chunks(int num_seqs, int T, int H, int passes, long long rows, b
     const double whole = packed ? std::max(longest + 6, (all + 6 * units) / S + 0.5 * longest)
                                 : std::ceil(units / S) * (mean + 6);
     double least = 0.9 * whole;
-    int best = 0;
+    LinCut best{0, false};
     for (int seg = 4; seg < longest; seg += 1 + seg / 16) {
-        const double walk = 1.7 * seg + 16;
-        const double cut = packed ? std::max(walk, (1.7 * all + 16 * units / (1 - std::exp(-seg / mean))) / S + 0.5 * walk) + 5
-                                  : std::ceil(units * std::ceil(mean / seg) / S) * walk + 5;
-        if (cut < least) {
-            least = cut;
-            best = seg;
+        const double count = units * (packed ? 1 / (1 - std::exp(-seg / mean)) : std::ceil(mean / seg));
+        for (int turns = 0; turns < 2; ++turns) {
+            if (turns && packed && num_seqs > TURN_SEQS) break;
+            const double rate = turns ? 1 : 1.7, start = turns ? 6 : 16, walk = rate * seg + start;
+            double cut = std::max(walk, (rate * all + start * count) / S + 0.5 * walk);
+            if (!packed) cut = turns ? std::max(cut, std::ceil(count / S) * walk) : std::ceil(count / S) * walk;
+            cut = turns ? std::max(cut, longest + start * std::ceil(longest / seg)) + 1 : cut + 5;
+            if (cut < least) {
+                least = cut;
+                best = LinCut{seg, turns != 0};
+            }
         }
     }
     return best;

@@ -49,6 +49,76 @@ __device__ __forceinline__ Work lin_work(const LinRun &a, int unit)
     return w;
 }
 
+// Segments in turn: the ticket's one, by the whole block.  Segments are given out by what their sequence has yet to
+// walk (its last segments count 1), the longest first, which fills the SMs until the longest sequences end; a
+// sequence's earlier ones come before its later ones, so that the one that hands over a state is running or done
+// already.  `scratch` holds 2 * 32 words.  A slot of -1: no segment is left.
+constexpr int TURN_SEQS = 896;   // packed sequences at most: one to a thread
+__device__ __forceinline__ Work lin_turn(const LinRun &a, int h, int *scratch)
+{
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
+    const int tokens = a.seg_chunks * C, all = (int)((a.rows + tokens - 1) / tokens);
+    if (tid == 0) scratch[0] = atomicAdd(a.tickets + h, 1);
+    __syncthreads();
+    const int ticket = scratch[0];
+    int n = -1, part = 0;   // part: in time
+    if (!a.cu_seqlens) {
+        const int parts = max(1, (a.T + tokens - 1) / tokens);
+        part = ticket / a.num_seqs;
+        if (part < parts) n = ticket % a.num_seqs;
+        __syncthreads();
+    } else {
+        const int mine = tid < a.num_seqs ? min(max(1, (lin_len(a, tid) + tokens - 1) / tokens), all + 1) : 0;
+        // segments with `level` or more to walk, themselves included
+        auto sum = [&](int v, int buf) {
+            v = __reduce_add_sync(0xffffffffu, v);
+            if (lane == 0) scratch[32 * buf + warp] = v;
+            __syncthreads();
+            return __reduce_add_sync(0xffffffffu, lane < warps ? scratch[32 * buf + lane] : 0);
+        };
+        __syncthreads();
+        int lo = 0, hi = all + 2, above = 0, buf = 1;   // more than `ticket` at lo, `above` (no more) at hi
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1, cnt = sum(max(0, mine - mid + 1), buf);
+            buf ^= 1;
+            if (cnt > ticket) lo = mid;
+            else {
+                hi = mid;
+                above = cnt;
+            }
+        }
+        // the (ticket - above)-th sequence of lo segments or more
+        const unsigned has = __ballot_sync(0xffffffffu, mine >= lo && lo > 0);
+        if (lane == 0) scratch[32 * buf + warp] = __popc(has);
+        __syncthreads();
+        int before = __popc(has & ((1u << lane) - 1));
+        for (int w = 0; w < warp; ++w) before += scratch[32 * buf + w];
+        buf ^= 1;
+        if (tid == 0) scratch[32 * buf] = -1;
+        __syncthreads();
+        if ((has >> lane & 1) && before == ticket - above) {
+            scratch[32 * buf] = tid;
+            scratch[32 * buf + 1] = mine - lo;
+        }
+        __syncthreads();
+        n = scratch[32 * buf];
+        part = scratch[32 * buf + 1];
+        __syncthreads();
+    }
+    Work w{};
+    w.slot = -1;
+    if (n < 0) return w;
+    w.n = n;
+    w.row0 = lin_row0(a, n);
+    w.len = lin_len(a, n);
+    w.nall = max(0, (w.len + C - 1) / C);
+    const int j = a.reverse ? max(1, (w.nall + a.seg_chunks - 1) / a.seg_chunks) - 1 - part : part;
+    w.slot = n + w.row0 / tokens + j;
+    w.c0 = j * a.seg_chunks;
+    w.nch = min(a.seg_chunks, w.nall - w.c0);
+    return w;
+}
+
 // Descriptors (low words): K step kk of a K-major tile in panels of 64 elements, and of an MN-major
 // [token][channel] tile in panels of 64 channels; `base` the tile's own.
 __device__ __forceinline__ uint32_t k_tile(uint32_t saddr) { return desc_sw128_lo(saddr, 16); }

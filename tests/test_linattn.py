@@ -13,6 +13,7 @@ a product of sums over channels; gate_sum_size adds up their magnitudes (and tho
 are a part of).
 """
 import math
+from types import SimpleNamespace
 
 import pytest
 import torch
@@ -456,6 +457,69 @@ def test_the_long_cases_are_cut(kda, c):
 def test_cut_sequences(kda, c):
     check_fwd(kda, make(21, *((DT[c[0]],) + c[1:]), rate=0.3), states=True)
     check_bwd(kda, make(22, *((DT[c[0]],) + c[1:]), rate=0.3))
+
+
+TURNS = [  # segments walked in turn, where (sequence, head) pairs do not fill whole waves of CTAs: B, T, Hk, H, dk, dv,
+    # cu, init; forward the first two and the third, backward the others
+    (3, 2048, 50, 50, 64, 64, None, True),
+    (3, 2047, 25, 50, 128, 64, None, False),
+    (1, 10000, 64, 64, 64, 128, [0, 0, 6200, 10000], True),
+    (1, 2500, 64, 64, 64, 64, None, True),
+    (1, 2500, 40, 80, 64, 128, None, False),
+    (1, 12000, 24, 24, 64, 64, [0, 7003, 12000], True),
+]
+
+
+def test_the_many_pairs_are_cut(kda):
+    for c in TURNS[:3]:
+        assert_cut(kda, ("bf16",) + c)
+
+
+@gpu
+@pytest.mark.parametrize("c", TURNS, ids=str)
+def test_segments_in_turn(kda, c):
+    """The last key head's value heads of a call with many."""
+    B, T, Hk, H, dk, dv, cu, init = c
+    x = make(25, torch.bfloat16, B, T, Hk, H, dk, dv, cu, init, rate=0.3)
+    d = dev(x)
+    fwd = lambda **kw: kda.kda_linattn_chunk_fwd(  # noqa: E731
+        d["q"], d["k"], d["v"], d["g"], cu_seqlens=d["cu"], initial_state=d["s0"], chunk_states=True, **kw)
+    bwd = lambda **kw: kda.kda_linattn_chunk_bwd(  # noqa: E731
+        d["q"], d["k"], d["v"], d["g"], d["do"], d["dsf"], cu_seqlens=d["cu"], initial_state=d["s0"], **kw)
+    f, b = fwd(), bwd()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    torch.cuda.synchronize()
+    again = [(fwd(stream=s), bwd(stream=s)) for s in streams]   # three at once, each with its own workspace
+    torch.cuda.synchronize()
+    for f2, b2 in again:
+        assert all(torch.equal(p, q) for p, q in zip(f[:2] + b, f2[:2] + b2))
+    hv, hk = slice(H - H // Hk, H), slice(Hk - 1, Hk)
+    y = {n: x[n] if x[n] is None or n == "cu" else x[n][:, :, hk] if n in "qk" else x[n][:, hv] if n in ("s0", "dsf")
+         else x[n][:, :, hv] for n in x}
+    part = (f[0][:, :, hv], f[1][:, hv], f[2][:, hv])
+    check_fwd(SimpleNamespace(kda_linattn_chunk_fwd=lambda *a, **kw: part, chunk_slot=kda.chunk_slot), y, states=True)
+    part = (b[0][:, :, hk], b[1][:, :, hk], b[2][:, :, hv], b[3][:, :, hv], b[4][:, hv])
+    check_bwd(SimpleNamespace(kda_linattn_chunk_bwd=lambda *a, **kw: part), y)
+
+
+@gpu
+def test_segments_in_turn_replayed(kda):
+    """Two graphs whose calls share nothing but the inputs, replayed in turn; the state written over in place."""
+    x = dev(make(26, torch.bfloat16, 3, 2048, 50, 50, 64, 64, init=True))
+    want, sf = kda.kda_linattn_chunk_fwd(x["q"], x["k"], x["v"], x["g"], initial_state=x["s0"])
+    state = x["s0"].clone()
+    graphs, outs = [], []
+    for _ in range(2):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            o, _ = kda.kda_linattn_chunk_fwd(x["q"], x["k"], x["v"], x["g"], initial_state=state, final_state=state)
+        graphs.append(graph), outs.append(o)
+    for _ in range(2):
+        for graph, o in zip(graphs, outs):
+            state.copy_(x["s0"]), o.zero_()
+            graph.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(o, want) and torch.equal(state, sf)
 
 
 @gpu
