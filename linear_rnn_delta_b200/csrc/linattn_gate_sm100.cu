@@ -6,8 +6,9 @@
 // Four products, D in tensor memory:  Q K^T and dO V^T (bf16 operands as loaded), and S_0 dO^T, G_C V^T
 // with lanes = key channels (in which the states are contiguous) and the state in three bf16 parts (2^-24), A from
 // tensor memory.  The rest is fp32: the inner products with q and k are lane sums, 32 tokens exchanged at once.
-// Bound by HBM: 2 states (8 d_k d_v bytes) and 4 tiles for each (chunk, head); two CTAs an SM cover each other's
-// latencies.
+// A chunk and head have 2 states (8 d_k d_v bytes) and 4 tiles to read.  What takes the time are the steps that wait for
+// one another (tiles, products, states, products): two CTAs an SM cover each other's, and 16 warps a CTA (8: 247 us)
+// shorten them.  4 x 4096 tokens, 16 heads, 128 x 128: 233 us, 2.9 TB/s.
 #include "linattn_sm100.cuh"
 
 namespace kda {
@@ -15,7 +16,8 @@ namespace {
 
 using namespace lin;
 
-constexpr int NT = 256;
+constexpr int NT = 512, ROWS = NT / 128;                 // warps of each quarter of the lanes
+constexpr int TW = C / ROWS;                             // tokens of a warp
 constexpr uint32_t SM_W = 4 * TILE;                      // q, k, dO, v tiles, then W [64][66]
 constexpr int WP = 66;                                   // W's row pitch
 constexpr uint32_t SM_END = SM_W + 64 * WP * 4;
@@ -40,7 +42,7 @@ __global__ void __launch_bounds__(NT, 2) lin_gate_kernel(const __grid_constant__
     __shared__ float2 s_c[C];
     __shared__ float s_win[C], s_uout[C], s_red[2][4][C], s_dq[C], s_dk[C], s_x[NT / 32], s_tot, s_pre[NT / 32][C];
     const LinGateGrad &a = P.a;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, quarter = warp & 3, half = warp >> 2;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, quarter = warp & 3, part_of = warp >> 2;
     const int slot = blockIdx.x / a.H, h = blockIdx.x % a.H;
     // sequence of the slot: the last one whose first slot is not behind it (first slots increase)
     int n = 0;
@@ -139,14 +141,14 @@ __global__ void __launch_bounds__(NT, 2) lin_gate_kernel(const __grid_constant__
         }
         finish();
         if (ok && quarter < 2) {   // row r of W, 32 columns
-            const int r = quarter * 32 + lane, s0 = half * 32;
-            float x[32], y[32];
-            tmem_ld32(tlane + TM_D + s0, x);
-            tmem_ld32(tlane + TM_S + s0, y);
+            const int r = quarter * 32 + lane, s0 = part_of * TW;
+            float x[TW], y[TW];
+            tmem_ld16(tlane + TM_D + s0, x);
+            tmem_ld16(tlane + TM_S + s0, y);
             tmem_wait_ld();
             const float2 cr = s_c[r];
 #pragma unroll
-            for (int e = 0; e < 32; ++e)
+            for (int e = 0; e < TW; ++e)
                 s_w[r * WP + s0 + e] = s0 + e < r ? x[e] * y[e] * ex2(diff(cr, s_c[s0 + e])) : 0.f;
         }
         tc_fence_before();
@@ -155,7 +157,7 @@ __global__ void __launch_bounds__(NT, 2) lin_gate_kernel(const __grid_constant__
     }
 
     // the two state products: S_0 with dO, weighed by q; G_C with v, weighed by k
-    const int i = quarter * 32 + lane, j0 = half * (DV / 2);
+    const int i = quarter * 32 + lane, j0 = part_of * (DV / ROWS);
     float accx = 0.f;
 #pragma unroll 1
     for (int m = 0; m < 2; ++m) {
@@ -167,7 +169,7 @@ __global__ void __launch_bounds__(NT, 2) lin_gate_kernel(const __grid_constant__
             const float *other = m == 0 && st1 ? st1 + (last ? (size_t)i * DV + j0 : (size_t)j0 * DK + i) : nullptr;
             const int step = nat ? 1 : DK, ostep = last ? 1 : DK;
 #pragma unroll 1
-            for (int b = 0; b < DV / 32; ++b) {   // 16 value channels
+            for (int b = 0; b < DV / ROWS / 16; ++b) {   // 16 value channels
                 float x[16], z[16];
 #pragma unroll
                 for (int e = 0; e < 16; ++e) x[e] = at[(b * 16 + e) * step];
@@ -204,29 +206,30 @@ __global__ void __launch_bounds__(NT, 2) lin_gate_kernel(const __grid_constant__
         }
         finish();
         if (ok) {
-            // this warp's 32 channels and 32 tokens: lane sums, halved and exchanged; lane l keeps token l
-            float y[32];
-            tmem_ld32(tlane + TM_D + half * 32, y);
+            // this warp's 32 channels and 16 tokens: lane sums, halved and exchanged; lanes 2 l, 2 l + 1 keep token l
+            float y[TW];
+            tmem_ld16(tlane + TM_D + part_of * TW, y);
             tmem_wait_ld();
             const uint8_t *tile = sm + m * TILE + (i >> 6) * 8192;
 #pragma unroll
-            for (int e = 0; e < 32; ++e) {
-                const int r = half * 32 + e;
+            for (int e = 0; e < TW; ++e) {
+                const int r = part_of * TW + e;
                 const unsigned short w = *reinterpret_cast<const unsigned short *>(tile + r * 128 + (((i & 63) * 2) ^ ((r & 7) << 4)));
                 y[e] = i < DK ? y[e] * __uint_as_float((uint32_t)w << 16) : 0.f;
             }
 #pragma unroll
-            for (int off = 16, cnt = 16; off; off >>= 1, cnt >>= 1) {
+            for (int off = 16, cnt = 8; cnt; off >>= 1, cnt >>= 1) {
                 const bool up = (lane & off) != 0;
 #pragma unroll
-                for (int e = 0; e < 16; ++e) {
+                for (int e = 0; e < 8; ++e) {
                     if (e < cnt) {
                         const float send = up ? y[e] : y[e + cnt], keep = up ? y[e + cnt] : y[e];
                         y[e] = keep + __shfl_xor_sync(0xffffffffu, send, off);
                     }
                 }
             }
-            s_red[m][quarter][half * 32 + lane] = y[0];
+            y[0] += __shfl_xor_sync(0xffffffffu, y[0], 1);
+            if (!(lane & 1)) s_red[m][quarter][part_of * TW + (lane >> 1)] = y[0];
         }
         tc_fence_before();
         __syncthreads();   // D and the parts are read
@@ -242,11 +245,11 @@ __global__ void __launch_bounds__(NT, 2) lin_gate_kernel(const __grid_constant__
         if (m == 0) s_dq[r] = r < nt && st0 ? s_win[r] * sum : 0.f;
         else s_dk[r] = r < nt && st1 ? s_uout[r] * sum : 0.f;
     }
-    {   // p_r(t) = sum_{s < t} W_rs, summed over the warp's 8 rows r >= t; a lane has t = 2 lane, 2 lane + 1
+    {   // p_r(t) = sum_{s < t} W_rs, summed over the warp's rows r >= t; a lane has t = 2 lane, 2 lane + 1
         float y0 = 0.f, y1 = 0.f;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const int r = warp * 8 + e;
+        for (int e = 0; e < C * 32 / NT; ++e) {
+            const int r = warp * (C * 32 / NT) + e;
             const float2 w = *reinterpret_cast<const float2 *>(s_w + r * WP + 2 * lane);
             float run = w.x + w.y;
 #pragma unroll
