@@ -11,7 +11,8 @@
 //
 // Bound by HBM: 5 bytes for each value in each direction.  A warp takes whole rows (16 bytes of state
 // and 4 bytes of codes for each lane), 4 of them in flight for each lane; the sum over a row's maximum
-// is a butterfly over the row's lanes.
+// is a butterfly over the row's lanes.  128 slots of 32 heads, 128 x 128 (335 MB each way): to int8 66 us (5.1 TB/s; a
+// branch for each value instead of one for four: 71), to e4m3 78 us, back 46 (58 from HBM alone).
 #include <cuda_fp8.h>
 
 #include "common.cuh"
@@ -34,33 +35,44 @@ __device__ __noinline__ int border_side(float ax, float amax, float top, float m
 // Adding 1.5 * 2^23 rounds to a whole number (ties to even) and leaves it in the low bits, in two's complement:
 // the conversion instructions run at a quarter of this rate and bound the kernel (91 against 51 us of traffic).
 constexpr float MAGIC = 12582912.f;
-// x TOP / A (inv = TOP / A) as an int8 code in the low byte
-__device__ __forceinline__ uint32_t int8_code(float x, float amax, float inv)
+// x TOP / A (inv = TOP / A) as an int8 code in the low byte of the result, and how far it is from it
+__device__ __forceinline__ uint32_t int8_code(float x, float inv, float &d)
+{
+    const float whole = fmaf(x, inv, MAGIC);
+    d = fabsf(fmaf(x, inv, MAGIC - whole));
+    return __float_as_uint(whole);
+}
+constexpr float INT8_NEAR = 0.5f - 6e-5f;   // inv is off by 2 units of 2^-23: 127 of those are 3e-5
+__device__ __noinline__ uint32_t int8_code_near(float x, float amax, float inv)
 {
     const float whole = fmaf(x, inv, MAGIC), r = whole - MAGIC, d = fmaf(x, inv, -r);
-    uint32_t code = __float_as_uint(whole);
-    if (fabsf(d) > 0.5f - 6e-5f) {   // inv is off by 2 units of 2^-23: 127 of those are 3e-5
-        const float m = fabsf(r + copysignf(0.5f, d));
-        const int side = border_side(fabsf(x), amax, 127.f, m);
-        const int below = (int)(m - 0.5f), mag = side < 0 ? below : side > 0 ? below + 1 : below + (below & 1);
-        code = (uint32_t)(x < 0.f ? -mag : mag);
-    }
-    return code & 0xffu;
+    if (fabsf(d) <= INT8_NEAR) return __float_as_uint(whole);
+    const float m = fabsf(r + copysignf(0.5f, d));
+    const int side = border_side(fabsf(x), amax, 127.f, m);
+    const int below = (int)(m - 0.5f), mag = side < 0 ? below : side > 0 ? below + 1 : below + (below & 1);
+    return (uint32_t)(x < 0.f ? -mag : mag);
 }
-// e4m3: a value that rounds (to nearest even) to the exact quotient's code
-__device__ __forceinline__ float e4m3_mag(float ax, float amax, float inv)
+// e4m3: |x| TOP / A, and whether it may be on the wrong side of a border between two codes
+__device__ __forceinline__ float e4m3_mag(float ax, float inv, bool &near)
 {
-    float t = ax * inv;
+    const float t = ax * inv, u = t * 512.f, r = (u + MAGIC) - MAGIC;
+    const uint32_t b = __float_as_uint(t);
+    // 3 stored bits, the border has the 20 below them at half; below 2^-6: steps of 2^-9.  t is off by 3 units at most
+    near |= t >= 0.015625f ? ((b + 0x80008u) & 0xFFFFFu) <= 16u : fabsf(u - r) > 0.5f - 1.6e-5f;
+    return t;
+}
+// a value that rounds (to nearest even) to the exact quotient's code
+__device__ __noinline__ float e4m3_mag_near(float ax, float amax, float inv)
+{
+    bool near = false;
+    const float t = e4m3_mag(ax, inv, near);
+    if (!near) return t;
     const uint32_t b = __float_as_uint(t);
     const float u = t * 512.f, r = (u + MAGIC) - MAGIC;
-    const bool normal = t >= 0.015625f;   // 3 stored bits, the border has the 20 below them at half; below: steps of 2^-9
-    const int d = (int)(b & 0xFFFFFu) - 0x80000;
-    if (normal ? d >= -8 && d <= 8 : fabsf(u - r) > 0.5f - 1.6e-5f) {   // t is off by 3 units at most
-        const float m = normal ? __uint_as_float((b & ~0xFFFFFu) | 0x80000u) : (r + copysignf(0.5f, u - r)) * (1.f / 512.f);
-        const int side = border_side(ax, amax, 448.f, m);
-        t = side == 0 ? m : __uint_as_float(__float_as_uint(m) + side);
-    }
-    return t;
+    const float m = t >= 0.015625f ? __uint_as_float((b & ~0xFFFFFu) | 0x80000u)
+                                   : (r + copysignf(0.5f, u - r)) * (1.f / 512.f);
+    const int side = border_side(ax, amax, 448.f, m);
+    return side == 0 ? m : __uint_as_float(__float_as_uint(m) + side);
 }
 
 // LPR lanes of a row (4 values each)
@@ -119,13 +131,30 @@ __global__ void __launch_bounds__(SC_NT) state_quantize_kernel(const StateCache 
                     for (int e = 0; e < 4; ++e) v[e] *= by;
                 }
                 const float inv = __fdividef(TOP, am);
+                // the four values' borders are looked at together: one branch, seldom taken
                 if (FMT == FMT_INT8) {
+                    uint32_t code[4];
+                    float d[4];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) word |= int8_code(v[e], am, inv) << (8 * e);
+                    for (int e = 0; e < 4; ++e) code[e] = int8_code(v[e], inv, d[e]);
+                    if (fmaxf(fmaxf(d[0], d[1]), fmaxf(d[2], d[3])) > INT8_NEAR) {
+#pragma unroll 1
+                        for (int e = 0; e < 4; ++e)
+                            word = word >> 8 | int8_code_near(e == 0 ? v[0] : e == 1 ? v[1] : e == 2 ? v[2] : v[3], am, inv) << 24;
+                    } else {
+                        word = __byte_perm(__byte_perm(code[0], code[1], 0x0040), __byte_perm(code[2], code[3], 0x0040), 0x5410);
+                    }
                 } else {
                     float t[4];
+                    bool near = false;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) t[e] = copysignf(e4m3_mag(fabsf(v[e]), am, inv), v[e]);
+                    for (int e = 0; e < 4; ++e) t[e] = e4m3_mag(fabsf(v[e]), inv, near);
+                    if (near) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) t[e] = e4m3_mag_near(fabsf(v[e]), am, inv);
+                    }
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) t[e] = copysignf(t[e], v[e]);
                     word = (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(t[0], t[1]), __NV_SATFINITE, __NV_E4M3) |
                            (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(t[2], t[3]), __NV_SATFINITE, __NV_E4M3) << 16;
                 }
