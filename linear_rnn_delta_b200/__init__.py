@@ -659,7 +659,8 @@ def kda_linattn_chunk_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: 
 class KdaLinAttnFunction(torch.autograd.Function):
     """Differentiable forward: ``KdaLinAttnFunction.apply(q, k, v, g,
     cu_seqlens, initial_state)`` returns (o, final_state) from
-    kda_linattn_chunk_fwd; the backward calls kda_linattn_chunk_bwd."""
+    kda_linattn_chunk_fwd; the backward calls kda_linattn_chunk_bwd and is
+    not differentiable itself."""
 
     @staticmethod
     def forward(ctx, q, k, v, g, cu_seqlens=None, initial_state=None):
@@ -669,6 +670,7 @@ class KdaLinAttnFunction(torch.autograd.Function):
         return o, sf
 
     @staticmethod
+    @torch.autograd.function.once_differentiable
     def backward(ctx, d_o, d_sf):
         q, k, v, g, cu_seqlens, initial_state = ctx.saved_tensors
         d_o = torch.zeros_like(v) if d_o is None else d_o.to(q.dtype).contiguous()

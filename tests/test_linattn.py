@@ -247,6 +247,29 @@ def test_values_behind_a_token_do_not_reach_it(kda, dtype, d):
 
 
 @gpu
+@pytest.mark.parametrize("dtype,dk,dv", [("bf16", 128, 128), ("bf16", 64, 128), ("bf16", 32, 64), ("fp32", 64, 64)])
+@pytest.mark.parametrize("name", ["q", "k", "v", "g", "do"])
+def test_neighbours_in_a_tile_stay_apart(kda, dtype, dk, dv, name):
+    """NaN in a document whose rows share 64-token tiles with the documents around it leaves their outputs, states
+    and gradients as they are."""
+    x = make(27, DT[dtype], 1, 300, 1, 2, dk, dv, cu=[0, 90, 190, 300], init=True)
+    y = dict(x)
+    y[name] = x[name].clone()
+    y[name][0, 90:190] = math.nan
+
+    def run(d):
+        d = dev(d)
+        return (kda.kda_linattn_chunk_fwd(d["q"], d["k"], d["v"], d["g"], cu_seqlens=d["cu"], initial_state=d["s0"]) +
+                kda.kda_linattn_chunk_bwd(d["q"], d["k"], d["v"], d["g"], d["do"], d["dsf"], cu_seqlens=d["cu"],
+                                          initial_state=d["s0"]))
+
+    for a, b in zip(run(x), run(y)):
+        rows = a.shape[0] != 3
+        for part in (slice(0, 90), slice(190, 300)) if rows else (slice(0, 1), slice(2, 3)):
+            assert torch.equal(a[0, part], b[0, part]) if rows else torch.equal(a[part], b[part])
+
+
+@gpu
 def test_empty_calls(kda):
     for dtype in (torch.bfloat16, torch.float32):
         x = dev(make(9, dtype, 2, 0, 1, 2, 64, 64, init=True))
@@ -322,6 +345,10 @@ def test_autograd_function(kda):
     (o.float() * d["do"].float()).sum().backward()
     want = kda.kda_linattn_chunk_bwd(d["q"], d["k"], d["v"], d["g"], d["do"], cu_seqlens=d["cu"])
     assert all(torch.equal(leaves[n].grad, w) for n, w in zip("qkvg", want))
+    o, _ = kda.KdaLinAttnFunction.apply(leaves["q"], leaves["k"], leaves["v"], leaves["g"], d["cu"], None)
+    first, = torch.autograd.grad((o.float() ** 2).sum(), leaves["q"], create_graph=True)
+    with pytest.raises(RuntimeError):   # the gradients have none of their own
+        first.float().sum().backward()
 
 
 def test_reference_gradients_are_differences():
