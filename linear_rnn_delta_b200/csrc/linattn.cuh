@@ -41,6 +41,11 @@ struct LinRun {
     int *tickets, *handed;
 };
 
+// Up to three passes of one shape, one cut of the token axis and one output type, side by side.
+struct LinRuns {
+    LinRun a[3];
+};
+
 __device__ __forceinline__ int lin_row0(const LinRun &a, int n) { return a.cu_seqlens ? a.cu_seqlens[n] : n * a.T; }
 __device__ __forceinline__ int lin_len(const LinRun &a, int n)
 {
@@ -62,10 +67,10 @@ struct LinGateGrad {
     const int32_t *cu_seqlens;
 };
 
-cudaError_t launch_lin_scan(const LinRun &r, int dx, int dz, bool bf16, cudaStream_t st);
-int lin_scan_segment_chunks(int num_seqs, int H, int dx, int dz, long long rows);   // chunks of a segment, as below
+cudaError_t launch_lin_scan(const LinRuns &r, int passes, int dx, int dz, bool bf16, cudaStream_t st);
+int lin_scan_segment_chunks(int num_seqs, int H, int passes, int dx, int dz, long long rows);   // chunks of a segment, as below
 // Turns what each segment adds (seg_state, seg_total) into the states that enter them.
-cudaError_t launch_lin_segments(const LinRun &r, int dx, int dz, cudaStream_t st);
+cudaError_t launch_lin_segments(const LinRuns &r, int passes, int dx, int dz, cudaStream_t st);
 // The tensor-core form's cut: chunks of a segment (0: sequences are left whole), and whether a sequence's segments
 // are walked in turn; and the segments' slots (segment j of sequence n is slot n + floor(R_n / tokens) + j, R_n its
 // first row).
@@ -80,8 +85,7 @@ inline int lin_segment_slots(int num_seqs, long long rows, int seg_chunks)
 }
 // Tensor-core form, bf16 only.
 bool lin_chunk_takes(int dx, int dz);
-// (1 to 3 passes of one shape, one cut of the token axis and one output type, side by side)
-cudaError_t launch_lin_chunk(const LinRun *r, int passes, int dx, int dz, cudaStream_t st);
+cudaError_t launch_lin_chunk(const LinRuns &r, int passes, int dx, int dz, cudaStream_t st);
 // Sums the per-value-head fp32 gradients over the heads that share a key head and casts them: dqf, dkf
 // [rows][H][dk]; dq, dk [rows][Hk][dk].
 cudaError_t launch_lin_share(const float *dqf, const float *dkf, void *dq, void *dk, long long rows, int Hk, int H,

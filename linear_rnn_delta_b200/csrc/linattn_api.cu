@@ -107,7 +107,7 @@ Segments segments(const LinSizes &s, int passes, bool chunk)
         g.chunks = cut.chunks;
         g.turns = cut.turns;
     } else {
-        g.chunks = kda::lin_scan_segment_chunks(s.N, s.H, s.dk, s.dv, s.rows);
+        g.chunks = kda::lin_scan_segment_chunks(s.N, s.H, passes, s.dk, s.dv, s.rows);
     }
     if (!g.chunks) return g;
     g.slots = kda::lin_segment_slots(s.N, s.rows, g.chunks);
@@ -136,14 +136,9 @@ cudaError_t launch_runs(LinRun *r, int passes, int dx, int dz, bool chunk, bool 
         const cudaError_t e = cudaMemsetAsync(seg_ws, 0, g.sync, st);
         if (e != cudaSuccess) return e;
     }
-    if (!chunk) {
-        for (int i = 0; i < passes; ++i) {
-            const cudaError_t e = kda::launch_lin_scan(r[i], dx, dz, bf16, st);
-            if (e != cudaSuccess) return e;
-        }
-        return cudaSuccess;
-    }
-    return kda::launch_lin_chunk(r, passes, dx, dz, st);
+    kda::LinRuns p{};
+    for (int i = 0; i < passes; ++i) p.a[i] = r[i];
+    return chunk ? kda::launch_lin_chunk(p, passes, dx, dz, st) : kda::launch_lin_scan(p, passes, dx, dz, bf16, st);
 }
 
 // Backward workspace regions.

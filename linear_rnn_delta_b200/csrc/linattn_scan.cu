@@ -56,8 +56,9 @@ __device__ __forceinline__ float4 load4(const __nv_bfloat16 *p)
 
 // STATE: only the state that a segment adds from nothing, and its decay.
 template <int DX, int DZ, typename TIn, bool STATE>
-__global__ void __launch_bounds__(LinScanShape<DX, DZ>::NTH) lin_scan_kernel(const LinRun a)
+__global__ void __launch_bounds__(LinScanShape<DX, DZ>::NTH) lin_scan_kernel(const __grid_constant__ LinRuns P)
 {
+    const LinRun &a = P.a[blockIdx.y];
     using SH = LinScanShape<DX, DZ>;
     constexpr int KS = SH::KS, CB = SH::CB, LIVE = SH::LIVE, NTH = SH::NTH, CTAS = SH::CTAS;
     __shared__ __align__(16) float s_x[2][STATE ? 1 : TB][DX], s_y[2][TB][DX], s_z[2][TB][CB];
@@ -311,53 +312,55 @@ __global__ void __launch_bounds__(LinScanShape<DX, DZ>::NTH) lin_scan_kernel(con
     }
 }
 
-template <int DX, int DZ, typename TIn> cudaError_t launch_type(const LinRun &r, cudaStream_t st)
+template <int DX, int DZ, typename TIn> cudaError_t launch_type(const LinRuns &p, int passes, cudaStream_t st)
 {
     using SH = LinScanShape<DX, DZ>;
+    const LinRun &r = p.a[0];
     const long long ctas = (long long)(r.seg_chunks ? r.slots : r.num_seqs) * r.H * SH::CTAS;
     if (ctas > 0x7fffffffll) return cudaErrorInvalidConfiguration;
+    const dim3 grid((unsigned)ctas, passes);
     if (r.seg_chunks) {
-        lin_scan_kernel<DX, DZ, TIn, true><<<(unsigned)ctas, SH::NTH, 0, st>>>(r);
+        lin_scan_kernel<DX, DZ, TIn, true><<<grid, SH::NTH, 0, st>>>(p);
         cudaError_t e = cudaGetLastError();
-        if (e != cudaSuccess || (e = launch_lin_segments(r, DX, DZ, st)) != cudaSuccess) return e;
+        if (e != cudaSuccess || (e = launch_lin_segments(p, passes, DX, DZ, st)) != cudaSuccess) return e;
     }
-    lin_scan_kernel<DX, DZ, TIn, false><<<(unsigned)ctas, SH::NTH, 0, st>>>(r);
+    lin_scan_kernel<DX, DZ, TIn, false><<<grid, SH::NTH, 0, st>>>(p);
     return cudaGetLastError();
 }
 template <int DX, int DZ>
-cudaError_t launch_dims(const LinRun &r, bool bf16, cudaStream_t st)
+cudaError_t launch_dims(const LinRuns &p, int passes, bool bf16, cudaStream_t st)
 {
-    return bf16 ? launch_type<DX, DZ, __nv_bfloat16>(r, st) : launch_type<DX, DZ, float>(r, st);
+    return bf16 ? launch_type<DX, DZ, __nv_bfloat16>(p, passes, st) : launch_type<DX, DZ, float>(p, passes, st);
 }
 template <int DX>
-cudaError_t launch_dz(const LinRun &r, int dz, bool bf16, cudaStream_t st)
+cudaError_t launch_dz(const LinRuns &p, int passes, int dz, bool bf16, cudaStream_t st)
 {
     switch (dz) {
-    case 16: return launch_dims<DX, 16>(r, bf16, st);
-    case 32: return launch_dims<DX, 32>(r, bf16, st);
-    case 64: return launch_dims<DX, 64>(r, bf16, st);
-    case 128: return launch_dims<DX, 128>(r, bf16, st);
+    case 16: return launch_dims<DX, 16>(p, passes, bf16, st);
+    case 32: return launch_dims<DX, 32>(p, passes, bf16, st);
+    case 64: return launch_dims<DX, 64>(p, passes, bf16, st);
+    case 128: return launch_dims<DX, 128>(p, passes, bf16, st);
     }
     return cudaErrorInvalidValue;
 }
 
 }  // namespace
 
-int lin_scan_segment_chunks(int num_seqs, int H, int dx, int dz, long long rows)
+int lin_scan_segment_chunks(int num_seqs, int H, int passes, int dx, int dz, long long rows)
 {
     // An SM holds 8 CTAs of 128 threads and needs about 4 to hide their latencies.  Cut, a token costs 5/3.
-    const double ctas = (double)num_seqs * H * std::max(1, dx * dz / 4096), chunks = (double)(rows + 63) / 64 / num_seqs;
+    const double ctas = (double)num_seqs * H * passes * std::max(1, dx * dz / 4096), chunks = (double)(rows + 63) / 64 / num_seqs;
     const double wanted = std::min(chunks, 4 * 148 / ctas);
     return wanted < 3 ? 0 : (int)std::max(1.0, std::ceil(chunks / wanted));
 }
 
-cudaError_t launch_lin_scan(const LinRun &r, int dx, int dz, bool bf16, cudaStream_t st)
+cudaError_t launch_lin_scan(const LinRuns &r, int passes, int dx, int dz, bool bf16, cudaStream_t st)
 {
     switch (dx) {
-    case 16: return launch_dz<16>(r, dz, bf16, st);
-    case 32: return launch_dz<32>(r, dz, bf16, st);
-    case 64: return launch_dz<64>(r, dz, bf16, st);
-    case 128: return launch_dz<128>(r, dz, bf16, st);
+    case 16: return launch_dz<16>(r, passes, dz, bf16, st);
+    case 32: return launch_dz<32>(r, passes, dz, bf16, st);
+    case 64: return launch_dz<64>(r, passes, dz, bf16, st);
+    case 128: return launch_dz<128>(r, passes, dz, bf16, st);
     }
     return cudaErrorInvalidValue;
 }

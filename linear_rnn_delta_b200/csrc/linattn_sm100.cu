@@ -734,8 +734,9 @@ constexpr int SEG_AHEAD = 8;
 
 // The states that enter the segments, in place of what each adds: one pass over a sequence's segments in time.
 // A thread has 4 values of one (sequence, head)'s state.
-__global__ void __launch_bounds__(256) lin_segment_kernel(const LinRun a, int dx, int dz)
+__global__ void __launch_bounds__(256) lin_segment_kernel(const __grid_constant__ LinRuns P, int dx, int dz)
 {
+    const LinRun &a = P.a[blockIdx.z];
     const int nh = blockIdx.x, n = nh / a.H, h = nh % a.H, size = dx * dz;
     const int e = (blockIdx.y * 256 + threadIdx.x) * 4;
     if (e >= size) return;
@@ -807,26 +808,24 @@ cudaError_t launch_kernel(const LinChunkParams &p, cudaStream_t st)
     return cudaGetLastError();
 }
 
-template <int DX, int DZ> cudaError_t launch_dims(const LinRun *r, int passes, cudaStream_t st)
+template <int DX, int DZ> cudaError_t launch_dims(const LinRuns &r, int passes, cudaStream_t st)
 {
     LinChunkParams p;
-    cudaError_t e = make_params<DX, DZ>(p, r, passes);
+    cudaError_t e = make_params<DX, DZ>(p, r.a, passes);
     if (e != cudaSuccess) return e;
-    if (r->seg_chunks && !r->tickets) {
+    if (r.a[0].seg_chunks && !r.a[0].tickets) {
         if ((e = launch_kernel<DX, DZ, true, false>(p, st)) != cudaSuccess) return e;
-        for (int i = 0; i < passes; ++i) {
-            if ((e = launch_lin_segments(r[i], DX, DZ, st)) != cudaSuccess) return e;
-        }
+        if ((e = launch_lin_segments(r, passes, DX, DZ, st)) != cudaSuccess) return e;
     }
     // passes of one launch have outputs of one type
-    return r->out_f32 ? launch_kernel<DX, DZ, false, true>(p, st) : launch_kernel<DX, DZ, false, false>(p, st);
+    return r.a[0].out_f32 ? launch_kernel<DX, DZ, false, true>(p, st) : launch_kernel<DX, DZ, false, false>(p, st);
 }
 
 }  // namespace
 
-cudaError_t launch_lin_segments(const LinRun &r, int dx, int dz, cudaStream_t st)
+cudaError_t launch_lin_segments(const LinRuns &r, int passes, int dx, int dz, cudaStream_t st)
 {
-    lin_segment_kernel<<<dim3(r.num_seqs * r.H, (dx * dz + 1023) / 1024), 256, 0, st>>>(r, dx, dz);
+    lin_segment_kernel<<<dim3(r.a[0].num_seqs * r.a[0].H, (dx * dz + 1023) / 1024, passes), 256, 0, st>>>(r, dx, dz);
     return cudaGetLastError();
 }
 
@@ -871,7 +870,7 @@ LinCut lin_cut(int num_seqs, int T, int H, int passes, long long rows, bool pack
     return best;
 }
 
-cudaError_t launch_lin_chunk(const LinRun *r, int passes, int dx, int dz, cudaStream_t st)
+cudaError_t launch_lin_chunk(const LinRuns &r, int passes, int dx, int dz, cudaStream_t st)
 {
     if (dx == 128 && dz == 128) return launch_dims<128, 128>(r, passes, st);
     if (dx == 128 && dz == 64) return launch_dims<128, 64>(r, passes, st);
