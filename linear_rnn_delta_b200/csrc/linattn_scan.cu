@@ -29,6 +29,7 @@ namespace kda {
 namespace {
 
 using lin::fix_exp2;
+using lin::fix_exp2_steady;
 using lin::fix_log2;
 
 constexpr int TB = 8;    // tokens of a block
@@ -157,11 +158,11 @@ __global__ void __launch_bounds__(LinScanShape<DX, DZ>::NTH) lin_scan_kernel(con
             const bool fits = L < NARROW && -L < NARROW && !nan;
             const bool wide = __any_sync(0xffffffffu, tid < TB && !fits);
             if (tid < TB) {
-                s_dec[buf][tid] = wide ? (nan ? pg : fix_exp2(f)) : 1.f;
+                s_dec[buf][tid] = wide ? (nan ? pg : fix_exp2_steady(f)) : 1.f;
                 s_in[buf][tid] = wide ? 1.f : fix_exp2(-L);
                 s_out[buf][tid] = wide ? 1.f : fix_exp2(L);
                 if (tid == TB - 1) {
-                    s_end[buf] = wide ? 1.f : fix_exp2(L);
+                    s_end[buf] = wide ? 1.f : fix_exp2_steady(L);
                     s_wide[buf] = wide;
                 }
                 if (STATE) {

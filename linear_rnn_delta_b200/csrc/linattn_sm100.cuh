@@ -181,6 +181,25 @@ __device__ __forceinline__ float fix_exp2(long long x)
     const float by = n < -126 ? 0.f : __int_as_float(n > 127 ? 0x7f800000 : (n + 127) << 23);
     return ex2(fix_rest(x)) * by;
 }
+// The same within 0.6 units in the last place, for the factors that a state is multiplied with again and again: with a
+// steady decay the same error compounds (ex2 is off by up to 2 units).  e^x - 1 = x (1 + x/2 (1 + x/3 (...))) with
+// x = ln 2 times the rest, |x| < 0.347, to x^8: what follows is below 2^-28.
+__device__ __forceinline__ float fix_exp2_steady(long long x)
+{
+    const int n = fix_int(x);
+    const float by = n < -126 ? 0.f : __int_as_float(n > 127 ? 0x7f800000 : (n + 127) << 23);
+    const float f = fix_rest(x), hi = f * 0.693147182f, lo = fmaf(f, 0.693147182f, -hi) - f * 1.90465421e-9f;
+    float y = 1.f / 40320.f;
+    y = fmaf(y, hi, 1.f / 5040.f);
+    y = fmaf(y, hi, 1.f / 720.f);
+    y = fmaf(y, hi, 1.f / 120.f);
+    y = fmaf(y, hi, 1.f / 24.f);
+    y = fmaf(y, hi, 1.f / 6.f);
+    y = fmaf(y, hi, 0.5f);
+    // 1 + (hi + (lo + hi^2 y)), lo's own powers below 2^-25 of the last place
+    const float rest = fmaf(hi * hi, y, fmaf(lo, hi, lo)), sum = 1.f + hi;
+    return (sum + ((hi - (sum - 1.f)) + rest)) * by;
+}
 __device__ __forceinline__ float diff(float2 a, float2 b) { return (a.x - b.x) + (a.y - b.y); }
 
 // max of the magnitudes of two bf16 pairs, NaN if either is one
