@@ -372,10 +372,11 @@ int kda_decode_step(int variant, int gate_range, int dtype,
  */
 
 /*
- * kda_linattn_chunk_fwd -- whole sequences.  workspace: caller-owned, 16-byte
- * aligned, kda_linattn_chunk_fwd_workspace_size(...) bytes (with the call's
- * flags; 0: may be NULL), not read before it is written; two calls that may
- * overlap on the GPU need one each.
+ * kda_linattn_chunk_fwd -- whole sequences.  final_state may be
+ * initial_state; no other output may share memory with an input.  workspace:
+ * caller-owned, 16-byte aligned, kda_linattn_chunk_fwd_workspace_size(...)
+ * bytes (with the call's flags; 0: may be NULL), not read before it is written;
+ * two calls that may overlap on the GPU need one each.
  */
 size_t kda_linattn_chunk_fwd_workspace_size(int dtype, int B, int T, int Hk, int H, int d_k, int d_v,
                                             int has_cu_seqlens, int num_seqs, unsigned flags);
@@ -395,8 +396,9 @@ int kda_linattn_chunk_fwd(int dtype, int B, int T, int Hk, int H, int d_k, int d
  *   dq_t = S_t d_o_t,  dk_t = G_t v_t,  dv_t = G_t^T k_t,
  *   G_t = a_{t+1} G_{t+1} + q_t d_o_t^T,
  *   dg_t = sum_{r >= t} (q_r . dq_r - k_r . dk_r) + <S_T, dL/dS_T>.
- * At g_t = -infinity dg_t is 0, the slope of e^g there.  Deterministic.  workspace as above, kda_linattn_chunk_bwd_workspace_size
- * bytes.  Flags: KDA_FLAG_FORCE_SCAN.
+ * At g_t = -infinity dg_t is 0, the slope of e^g there.  Deterministic.  No
+ * output may share memory with an input.  workspace as above,
+ * kda_linattn_chunk_bwd_workspace_size bytes.  Flags: KDA_FLAG_FORCE_SCAN.
  */
 size_t kda_linattn_chunk_bwd_workspace_size(int dtype, int B, int T, int Hk, int H, int d_k, int d_v,
                                             int has_cu_seqlens, int num_seqs);

@@ -266,6 +266,9 @@ extern "C" int kda_linattn_chunk_bwd(int dtype, int B, int T, int Hk, int H, int
     CHECK(opt_ptr(initial_state, "initial_state"));
     CHECK(opt_ptr(d_final_state, "d_final_state"));
     CHECK(opt_ptr(d_initial_state, "d_initial_state"));
+    // both are read after d_initial_state is written
+    if (d_initial_state && (d_initial_state == d_final_state || d_initial_state == initial_state))
+        return fail(KDA_ERR_INVALID_ARG, "d_initial_state is d_final_state or initial_state");
     const bool chunk = chunk_form(s, flags);
     const BwdLayout L = bwd_layout(s, chunk);
     if (!workspace || !aligned16(workspace) || workspace_bytes < L.total)

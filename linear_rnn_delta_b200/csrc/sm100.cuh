@@ -285,18 +285,8 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t *u)
                  :: "r"(taddr), "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7])
                  : "memory");
 }
-// 16 lanes x 32 columns from the fragments of eight 16x(4 columns) pieces: u[2k] is lane t/4, column 4k + t%4,
+// 16 lanes x 16 columns from the fragments of four 16x(4 columns) pieces: u[2k] is lane t/4, column 4k + t%4,
 // u[2k+1] the same column of lane t/4 + 8
-__device__ __forceinline__ void tmem_st_frag8(uint32_t taddr, const uint32_t *u)
-{
-    asm volatile(
-        "tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], "
-        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
-        :: "r"(taddr), "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7]),
-           "r"(u[8]), "r"(u[9]), "r"(u[10]), "r"(u[11]), "r"(u[12]), "r"(u[13]), "r"(u[14]), "r"(u[15])
-        : "memory");
-}
-// ... 16 columns, four pieces
 __device__ __forceinline__ void tmem_st_frag4(uint32_t taddr, const uint32_t *u)
 {
     asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"

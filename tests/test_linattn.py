@@ -13,6 +13,10 @@ a product of sums over channels; gate_sum_size adds up their magnitudes (and tho
 are a part of).
 """
 import math
+import subprocess
+import sys
+import threading
+from pathlib import Path
 from types import SimpleNamespace
 
 import pytest
@@ -192,6 +196,17 @@ def test_long_sequences_cross_the_gate_segments(kda, dtype, T):
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 def test_packed_segments(kda, dtype):
     x = make(5, DT[dtype], 1, 1300, 1, 2, 64, 64, cu=[0, 3, 700, 700, 1300], init=True, rate=0.1)
+    check_fwd(kda, x, states=True)
+    check_bwd(kda, x)
+
+
+@gpu
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_many_documents(kda, dtype):
+    """1000 documents of 0 to 9 tokens, more than a block's threads and several to a tile."""
+    gen = torch.Generator().manual_seed(29)
+    cu = [0] + torch.randint(0, 10, (1000,), generator=gen).cumsum(0).tolist()
+    x = make(29, DT[dtype], 1, cu[-1], 1, 1, 64, 64, cu=cu, init=True)
     check_fwd(kda, x, states=True)
     check_bwd(kda, x)
 
@@ -400,6 +415,55 @@ def test_graph_replay(kda):
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+FIRST = """
+import sys, torch, linear_rnn_delta_b200 as kda
+torch.manual_seed(0)
+dt, what = getattr(torch, sys.argv[1]), sys.argv[2]
+q, k, v, do = [torch.randn(1, 300, 2, 128, device="cuda").to(dt) for _ in range(4)]
+g = -0.1 * torch.rand(1, 300, 2, device="cuda")
+calls = dict(fwd=lambda: kda.kda_linattn_chunk_fwd(q, k, v, g), bwd=lambda: kda.kda_linattn_chunk_bwd(q, k, v, g, do)[:4],
+             step=lambda: [kda.kda_linattn_decode_step(q[0], k[0], v[0], g[0], torch.zeros(300, 2, 128, 128, device="cuda"))])
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    got = calls[what]()
+graph.replay()
+assert all(torch.equal(a, b) for a, b in zip(got, calls[what]()))
+"""
+
+
+@gpu
+@pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
+@pytest.mark.parametrize("what", ["fwd", "bwd", "step"])
+def test_the_first_call_may_be_captured(dtype, what):
+    """In a process that has launched nothing of the library yet."""
+    run = subprocess.run([sys.executable, "-c", FIRST, dtype, what], cwd=Path(__file__).parents[1], capture_output=True, text=True,
+                         timeout=300)
+    assert run.returncode == 0, run.stderr[-2000:]
+
+
+@gpu
+def test_calls_from_threads(kda):
+    x = dev(make(28, torch.bfloat16, 1, 300, 2, 2, 128, 128))
+    args = (x["q"], x["k"], x["v"], x["g"])
+    want = kda.kda_linattn_chunk_fwd(*args) + kda.kda_linattn_chunk_bwd(*args, x["do"])[:4]
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work():
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for _ in range(10):
+                got = kda.kda_linattn_chunk_fwd(*args) + kda.kda_linattn_chunk_bwd(*args, x["do"])[:4]
+            torch.cuda.current_stream().synchronize()
+            wrong.extend(not torch.equal(a, b) for a, b in zip(got, want))
+
+    threads = [threading.Thread(target=work) for _ in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert len(wrong) == 4 * len(want) and not any(wrong)
 
 
 @gpu
@@ -651,7 +715,7 @@ def test_abi_refuses(kda):
             assert f(**bad) == 1, (f, bad)
     assert fwd(o=None) == 1 and fwd(o=BAD) == 1 and fwd(sf=BAD) == 1 and fwd(cs=BAD) == 1
     for bad in (dict(do=None), dict(do=BAD), dict(dsf=BAD), dict(dq=None), dict(dk_=BAD), dict(dv_=None), dict(dg=None), dict(dg=ODD),
-                dict(ds0=BAD), dict(ws=None), dict(wsb=64), dict(flags=1)):
+                dict(ds0=BAD), dict(ws=None), dict(wsb=64), dict(flags=1), dict(ds0=P, dsf=P), dict(ds0=P, s0=P)):
         assert bwd(**bad) == 1, bad
     assert dec(N=0) == 1 and dec(state=None) == 1 and dec(state=BAD) == 1 and dec(o=None) == 1 and dec(flags=2) == 1
     size = lib.kda_linattn_chunk_bwd_workspace_size
