@@ -32,9 +32,10 @@ struct LinRun {
     int num_seqs, T, H;
     const int32_t *cu_seqlens;  // packed batch, or NULL (sequence n is rows n*T .. n*T+T-1)
     long long rows;             // tokens of the whole batch
-    // token axis in segments: chunks of 64 tokens of one (0: not cut), slots of all sequences, and the state
+    // token axis in segments: chunks of one (of 64 tokens, the scan's of 16; 0: not cut) and tokens, slots of all
+    // sequences, and the state
     // that enters each slot's segment [slot][H][d_x][d_z] with the decay over it [slot][H]
-    int seg_chunks, slots;
+    int seg_chunks, seg_tokens, slots;
     float *seg_state, *seg_total;
     // segments in turn (tensor-core form): tickets given out [H] and state hand-overs done [slot][H], zero at the
     // launch; NULL: side by side
@@ -68,7 +69,8 @@ struct LinGateGrad {
 };
 
 cudaError_t launch_lin_scan(const LinRuns &r, int passes, int dx, int dz, bool bf16, cudaStream_t st);
-int lin_scan_segment_chunks(int num_seqs, int H, int passes, int dx, int dz, long long rows);   // chunks of a segment, as below
+constexpr int SCAN_CHUNK = 16;
+int lin_scan_segment_chunks(int num_seqs, int H, int passes, int dx, int dz, long long rows);   // of SCAN_CHUNK, as below
 // Turns what each segment adds (seg_state, seg_total) into the states that enter them.
 cudaError_t launch_lin_segments(const LinRuns &r, int passes, int dx, int dz, cudaStream_t st);
 // The tensor-core form's cut: chunks of a segment (0: sequences are left whole), and whether a sequence's segments
@@ -79,9 +81,9 @@ struct LinCut {
     bool turns;
 };
 LinCut lin_cut(int num_seqs, int T, int H, int passes, long long rows, bool packed);
-inline int lin_segment_slots(int num_seqs, long long rows, int seg_chunks)
+inline int lin_segment_slots(int num_seqs, long long rows, int seg_tokens)
 {
-    return (int)(num_seqs + (rows + seg_chunks * 64 - 1) / (seg_chunks * 64));
+    return (int)(num_seqs + (rows + seg_tokens - 1) / seg_tokens);
 }
 // Tensor-core form, bf16 only.
 bool lin_chunk_takes(int dx, int dz);

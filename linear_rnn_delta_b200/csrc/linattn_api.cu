@@ -93,7 +93,7 @@ bool chunk_form(const LinSizes &s, unsigned flags)
 }
 // Segments of the token axis: their length and the workspace of a pass's states and decays.
 struct Segments {
-    int chunks, slots;
+    int chunks, tokens, slots;
     bool turns;
     size_t sync;            // bytes of all passes' tickets and hand-overs, first in the workspace
     size_t totals, total;   // a pass's offset and size in bytes
@@ -110,7 +110,8 @@ Segments segments(const LinSizes &s, int passes, bool chunk)
         g.chunks = kda::lin_scan_segment_chunks(s.N, s.H, passes, s.dk, s.dv, s.rows);
     }
     if (!g.chunks) return g;
-    g.slots = kda::lin_segment_slots(s.N, s.rows, g.chunks);
+    g.tokens = g.chunks * (chunk ? kda::SLOT_TOKENS : kda::SCAN_CHUNK);
+    g.slots = kda::lin_segment_slots(s.N, s.rows, g.tokens);
     g.sync = g.turns ? up256((size_t)passes * (1 + g.slots) * s.H * 4) : 0;
     g.totals = up256((size_t)g.slots * s.H * s.dk * s.dv * 4);
     g.total = g.totals + (g.turns ? 0 : up256((size_t)g.slots * s.H * 4));
@@ -123,6 +124,7 @@ cudaError_t launch_runs(LinRun *r, int passes, int dx, int dz, bool chunk, bool 
 {
     for (int i = 0; g.chunks && i < passes; ++i) {
         r[i].seg_chunks = g.chunks;
+        r[i].seg_tokens = g.tokens;
         r[i].slots = g.slots;
         r[i].seg_state = reinterpret_cast<float *>(seg_ws + g.sync + i * g.total);
         if (g.turns) {

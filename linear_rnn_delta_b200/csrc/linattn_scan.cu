@@ -18,7 +18,8 @@
 // without a token have x = y = z = 0 and no decay: they leave the state as it is.
 // Bound by issue: 8 packed multiply-adds, 5 16-byte shared loads and 4 shuffles a token for 32 elements a lane.  One
 // warp an SM sub-partition takes 200 ns a token, so few (sequence, head) pairs are cut into segments, like the
-// chunk form's: their states first (two thirds of the work), then all segments side by side.
+// chunk form's: their states first (two thirds of the work), then all segments side by side.  2 x 300 tokens, 2 heads,
+// 32 x 64: 4 and 6 us in segments of 16 tokens (of 64: 9 and 15); 2 x 1001, 8 heads, 64 x 128: 19 and 41 us.
 #include <algorithm>
 #include <cmath>
 #include <mutex>
@@ -68,7 +69,7 @@ __global__ void __launch_bounds__(LinScanShape<DX, DZ>::NTH) lin_scan_kernel(con
 
     const int pair = blockIdx.x / CTAS, cblk = blockIdx.x % CTAS;
     const int h = pair % a.H;
-    const lin::Work work = lin::lin_work(a, pair / a.H);
+    const lin::Work work = lin::lin_work<SCAN_CHUNK>(a, pair / a.H);
     if (a.seg_chunks && work.nch <= 0) return;
     const bool rev = a.reverse != 0;
     const bool closing = rev ? work.c0 == 0 : work.c0 + work.nch == work.nall;   // the sequence's last segment in time
@@ -78,7 +79,7 @@ __global__ void __launch_bounds__(LinScanShape<DX, DZ>::NTH) lin_scan_kernel(con
     const int p = tid % KS, grp = live ? tid / KS : 0;
     const int j = cblk * CB + grp * 4;                 // first of the group's columns
     const int n = work.n, row0 = work.row0, len = work.len;
-    const int beg = work.c0 * lin::C, end = min(len, beg + work.nch * lin::C);   // the segment's tokens
+    const int beg = work.c0 * SCAN_CHUNK, end = min(len, beg + work.nch * SCAN_CHUNK);   // the segment's tokens
     const int hx = a.H / a.gx, hy = a.H / a.gy, hz = a.H / a.gz;
     const TIn *x = (const TIn *)a.x + (size_t)(h / a.gx) * DX, *y = (const TIn *)a.y + (size_t)(h / a.gy) * DX;
     const TIn *z = (const TIn *)a.z + (size_t)(h / a.gz) * DZ + cblk * CB;
@@ -105,7 +106,7 @@ __global__ void __launch_bounds__(LinScanShape<DX, DZ>::NTH) lin_scan_kernel(con
     float pg = 0.f;
     long long sum = 0;   // STATE: this lane's share of the segment's log-decays
     bool any_nan = false;
-    const int nblk = (end - beg + TB - 1) / TB;          // beg is a multiple of 64
+    const int nblk = (end - beg + TB - 1) / TB;          // beg is a multiple of TB
     // token of step u of the b-th block in time
     auto token = [&](int b, int u) { return rev ? beg + (nblk - 1 - b) * TB + TB - 1 - u : beg + b * TB + u; };
     auto fetch = [&](int b) {
@@ -349,8 +350,10 @@ cudaError_t launch_dz(const LinRuns &p, int passes, int dz, bool bf16, cudaStrea
 
 int lin_scan_segment_chunks(int num_seqs, int H, int passes, int dx, int dz, long long rows)
 {
-    // An SM holds 8 CTAs of 128 threads and needs about 4 to hide their latencies.  Cut, a token costs 5/3.
-    const double ctas = (double)num_seqs * H * passes * std::max(1, dx * dz / 4096), chunks = (double)(rows + 63) / 64 / num_seqs;
+    // An SM holds 8 CTAs of 128 threads and needs about 4 to hide their latencies.  Cut, a token costs 5/3, and a
+    // segment's two walks a start of 2 us each (10 tokens): not shorter than 16 tokens.
+    const double ctas = (double)num_seqs * H * passes * std::max(1, dx * dz / 4096);
+    const double chunks = (double)(rows + SCAN_CHUNK - 1) / SCAN_CHUNK / num_seqs;
     const double wanted = std::min(chunks, 4 * 148 / ctas);
     return wanted < 3 ? 0 : (int)std::max(1.0, std::ceil(chunks / wanted));
 }

@@ -740,7 +740,7 @@ __global__ void __launch_bounds__(256) lin_segment_kernel(const __grid_constant_
     const int nh = blockIdx.x, n = nh / a.H, h = nh % a.H, size = dx * dz;
     const int e = (blockIdx.y * 256 + threadIdx.x) * 4;
     if (e >= size) return;
-    const int row0 = lin_row0(a, n), len = lin_len(a, n), tokens = a.seg_chunks * C;
+    const int row0 = lin_row0(a, n), len = lin_len(a, n), tokens = a.seg_tokens;
     const int first = n + row0 / tokens, nseg = (len + tokens - 1) / tokens;
     float4 cur = make_float4(0.f, 0.f, 0.f, 0.f);
     if (a.s_in) {

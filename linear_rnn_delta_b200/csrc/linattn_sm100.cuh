@@ -22,11 +22,11 @@ constexpr long long WAIT_LIMIT = 1ll << 32;           // cycles, about 2 s (the 
 constexpr uint32_t WAIT_NS = 1000000, WAIT_POLLS = 2000;   // a poll sleeps for up to 1 ms: about 2 s
 constexpr unsigned DEV_WAIT_TIMEOUT = 1u;
 
-// What a CTA walks: chunks c0 .. c0 + nch - 1 of sequence n (nall in all; none: the slot is nobody's).
+// What a CTA walks, in chunks of U tokens: chunks c0 .. c0 + nch - 1 of sequence n (nall in all; none: the slot is nobody's).
 struct Work {
     int n, slot, row0, len, c0, nch, nall;
 };
-__device__ __forceinline__ Work lin_work(const LinRun &a, int unit)
+template <int U = C> __device__ __forceinline__ Work lin_work(const LinRun &a, int unit)
 {
     Work w;
     w.slot = unit;
@@ -34,7 +34,7 @@ __device__ __forceinline__ Work lin_work(const LinRun &a, int unit)
         int lo = 0, hi = a.num_seqs - 1;
         while (lo < hi) {
             const int mid = (lo + hi + 1) / 2;
-            if (mid + lin_row0(a, mid) / (a.seg_chunks * C) <= unit) lo = mid;
+            if (mid + lin_row0(a, mid) / a.seg_tokens <= unit) lo = mid;
             else hi = mid - 1;
         }
         w.n = lo;
@@ -43,8 +43,8 @@ __device__ __forceinline__ Work lin_work(const LinRun &a, int unit)
     }
     w.row0 = lin_row0(a, w.n);
     w.len = lin_len(a, w.n);
-    w.nall = (w.len + C - 1) / C;
-    w.c0 = a.seg_chunks ? (unit - w.n - w.row0 / (a.seg_chunks * C)) * a.seg_chunks : 0;
+    w.nall = (w.len + U - 1) / U;
+    w.c0 = a.seg_chunks ? (unit - w.n - w.row0 / a.seg_tokens) * a.seg_chunks : 0;
     w.nch = a.seg_chunks ? min(a.seg_chunks, w.nall - w.c0) : w.nall;
     return w;
 }
@@ -57,7 +57,7 @@ constexpr int TURN_SEQS = 896;   // packed sequences at most: one to a thread
 __device__ __forceinline__ Work lin_turn(const LinRun &a, int h, int *scratch)
 {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
-    const int tokens = a.seg_chunks * C, all = (int)((a.rows + tokens - 1) / tokens);
+    const int tokens = a.seg_tokens, all = (int)((a.rows + tokens - 1) / tokens);
     if (tid == 0) scratch[0] = atomicAdd(a.tickets + h, 1);
     __syncthreads();
     const int ticket = scratch[0];
