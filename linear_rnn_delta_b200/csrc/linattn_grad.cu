@@ -61,7 +61,7 @@ __global__ void __launch_bounds__(GT) lin_gate_chunk_kernel(const LinGateGrad a)
     float *s_s = s_v + GC * PV, *s_g = s_s + GROWS * PK;            // rows of S^T and G^T
     float *s_w = s_g + GROWS * PK;                                  // [64][65]
     __shared__ float2 s_c[GC];
-    __shared__ float s_win[GC], s_uout[GC], s_dq[GC], s_dk[GC], s_x[GT / 32], s_tot, s_part[2];
+    __shared__ float s_win[GC], s_uout[GC], s_dq[GC], s_dk[GC], s_x[GT / 32], s_tot, s_pre[GT / 32][GC];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int slot = blockIdx.x / a.H, h = blockIdx.x % a.H;
     // sequence of the slot: the last one whose first slot is not behind it (first slots increase)
@@ -212,45 +212,68 @@ __global__ void __launch_bounds__(GT) lin_gate_chunk_kernel(const LinGateGrad a)
     if (lane == 0) s_x[warp] = accx;
     __syncthreads();
 
-    // row prefixes of W: [r][t] = sum_{s < t} W_rs
-    if (tid < GC) {
-        float run = 0.f;
-        for (int s = 0; s < GC; ++s) {
-            const float w = s_w[tid * 65 + s];
-            s_w[tid * 65 + s] = run;
-            run += w;
+    {   // p_r(t) = sum_{s < t} W_rs, summed over the warp's 8 rows r >= t; a lane has t = 2 lane, 2 lane + 1
+        float y0 = 0.f, y1 = 0.f;
+#pragma unroll
+        for (int e = 0; e < GC * 32 / GT; ++e) {
+            const int r2 = warp * (GC * 32 / GT) + e;
+            const float w0 = s_w[r2 * 65 + 2 * lane], w1 = s_w[r2 * 65 + 2 * lane + 1];
+            float run = w0 + w1;
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const float o = __shfl_up_sync(0xffffffffu, run, off);
+                if (lane >= off) run += o;
+            }
+            float before = __shfl_up_sync(0xffffffffu, run, 1);
+            if (lane == 0) before = 0.f;
+            if (r2 >= 2 * lane && r2 < nt) y0 += before;
+            if (r2 >= 2 * lane + 1 && r2 < nt) y1 += before + w0;
         }
+        s_pre[warp][2 * lane] = y0;
+        s_pre[warp][2 * lane + 1] = y1;
     }
     __syncthreads();
-    if (tid < GC) {
-        const int t = tid;
-        float x = 0.f;
-        for (int r2 = GC - 1; r2 >= t; --r2) x += s_w[r2 * 65 + t];
-        float y = 0.f;
-        for (int r2 = nt - 1; r2 >= t; --r2) y += s_dq[r2];
-        float z = 0.f;
-        for (int s = 0; s < t; ++s) z += s_dk[s];
+    if (warp == 0) {   // t = 2 lane, 2 lane + 1
+        const int t = 2 * lane;
+        float x[2] = {0.f, 0.f};
+#pragma unroll
+        for (int w = 0; w < GT / 32; ++w) {
+            x[0] += s_pre[w][t];
+            x[1] += s_pre[w][t + 1];
+        }
+        const float q0 = s_dq[t], q1 = s_dq[t + 1], k0 = s_dk[t], k1 = s_dk[t + 1];
+        float after = q0 + q1, before = k0 + k1;   // sums of dq from t on, of dk up to t + 1
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const float o = __shfl_down_sync(0xffffffffu, after, off), u = __shfl_up_sync(0xffffffffu, before, off);
+            if (lane + off < 32) after += o;
+            if (lane >= off) before += u;
+        }
+        float sq = __shfl_down_sync(0xffffffffu, after, 1), sk = __shfl_up_sync(0xffffffffu, before, 1);
+        if (lane == 31) sq = 0.f;
+        if (lane == 0) sk = 0.f;
         float cross = 0.f;
         if (S0 && GC_) {
             for (int w = 0; w < GT / 32; ++w) cross += s_x[w];
             cross *= s_tot;
         }
-        x = (x + y) + (z + cross);
+        x[0] = (x[0] + (q0 + q1 + sq)) + (sk + cross);
+        x[1] = (x[1] + (q1 + sq)) + (sk + k0 + cross);
         float sum = 0.f;
-        if (t < nt) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            if (t + e >= nt) continue;
             // e^g has slope 0 at -infinity (the states' products may have an infinity's NaN there)
-            if (a.g[(row + t) * a.g_ld + h] == -INFINITY) x = 0.f;
-            if (a.dg) a.dg[(row + t) * a.H + h] = x;
-            sum = x;
+            if (a.g[(row + t + e) * a.g_ld + h] == -INFINITY) x[e] = 0.f;
+            if (a.dg) a.dg[(row + t + e) * a.H + h] = x[e];
+            sum += x[e];
         }
         if (a.partial) {
 #pragma unroll
             for (int off = 16; off; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-            if (lane == 0) s_part[warp] = sum;
+            if (lane == 0) a.partial[(size_t)slot * a.H + h] = sum;
         }
     }
-    __syncthreads();
-    if (a.partial && tid == 0) a.partial[(size_t)slot * a.H + h] = s_part[0] + s_part[1];
 }
 
 // dg of a head's own decay: the sum over its segments, in slot order and 64 bits
