@@ -14,6 +14,8 @@
 namespace kda {
 namespace {
 
+using lin::load4;
+
 // Sums the value heads' gradients of a shared key head, in head order; 4 channels a thread, 8 heads' loads in flight.
 // Bound by HBM: 8191 tokens of 16 heads over 2, 128 channels, 134 MB in 25 us (5.3 TB/s; one head after the other: 29 us).
 template <typename TOut>
@@ -88,15 +90,19 @@ __global__ void __launch_bounds__(GT) lin_gate_chunk_kernel(const LinGateGrad a)
     // tiles, zero behind the sequence's end
     const TIn *q = (const TIn *)a.q + (row * a.Hk + hk) * DK, *k = (const TIn *)a.k + (row * a.Hk + hk) * DK;
     const TIn *v = (const TIn *)a.v + (row * a.H + h) * DV, *d = (const TIn *)a.d_o + (row * a.H + h) * DV;
-    for (int e = tid; e < GC * DK; e += GT) {
-        const int r = e / DK, i = e % DK;
-        s_q[r * PK + i] = r < nt ? ld_f32(q + (size_t)r * a.Hk * DK + i) : 0.f;
-        s_k[r * PK + i] = r < nt ? ld_f32(k + (size_t)r * a.Hk * DK + i) : 0.f;
+#pragma unroll
+    for (int e = tid; e < GC * DK / 4; e += GT) {
+        const int r = e / (DK / 4), i = e % (DK / 4) * 4;
+        const bool in = r < nt;
+        *reinterpret_cast<float4 *>(s_q + r * PK + i) = in ? load4(q + (size_t)r * a.Hk * DK + i) : make_float4(0.f, 0.f, 0.f, 0.f);
+        *reinterpret_cast<float4 *>(s_k + r * PK + i) = in ? load4(k + (size_t)r * a.Hk * DK + i) : make_float4(0.f, 0.f, 0.f, 0.f);
     }
-    for (int e = tid; e < GC * DV; e += GT) {
-        const int r = e / DV, j = e % DV;
-        s_do[r * PV + j] = r < nt ? ld_f32(d + (size_t)r * a.H * DV + j) : 0.f;
-        s_v[r * PV + j] = r < nt ? ld_f32(v + (size_t)r * a.H * DV + j) : 0.f;
+#pragma unroll
+    for (int e = tid; e < GC * DV / 4; e += GT) {
+        const int r = e / (DV / 4), j = e % (DV / 4) * 4;
+        const bool in = r < nt;
+        *reinterpret_cast<float4 *>(s_do + r * PV + j) = in ? load4(d + (size_t)r * a.H * DV + j) : make_float4(0.f, 0.f, 0.f, 0.f);
+        *reinterpret_cast<float4 *>(s_v + r * PV + j) = in ? load4(v + (size_t)r * a.H * DV + j) : make_float4(0.f, 0.f, 0.f, 0.f);
     }
     if (warp == 0) {   // sums of log2-decays
         const float g0 = 2 * lane < nt ? a.g[(row + 2 * lane) * a.g_ld + h] : 0.f;

@@ -32,6 +32,7 @@ namespace {
 using lin::fix_exp2;
 using lin::fix_exp2_steady;
 using lin::fix_log2;
+using lin::load4;
 
 constexpr int TB = 8;    // tokens of a block
 constexpr int TU = 4;    // tokens whose sums are exchanged together
@@ -46,15 +47,6 @@ template <int DX, int DZ> struct LinScanShape {
     static constexpr int CTAS = DZ / CB;
     static_assert(NTH % 32 == 0 && (LIVE % 32 == 0 || LIVE < 32), "whole warps");
 };
-
-// 4 consecutive elements as fp32
-__device__ __forceinline__ float4 load4(const float *p) { return *reinterpret_cast<const float4 *>(p); }
-__device__ __forceinline__ float4 load4(const __nv_bfloat16 *p)
-{
-    const uint2 u = *reinterpret_cast<const uint2 *>(p);
-    return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u),
-                       __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xffff0000u));
-}
 
 // STATE: only the state that a segment adds from nothing, and its decay.
 template <int DX, int DZ, typename TIn, bool STATE>

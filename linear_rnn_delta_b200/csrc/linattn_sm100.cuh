@@ -119,6 +119,15 @@ __device__ __forceinline__ Work lin_turn(const LinRun &a, int h, int *scratch)
     return w;
 }
 
+// 4 consecutive elements as fp32
+__device__ __forceinline__ float4 load4(const float *p) { return *reinterpret_cast<const float4 *>(p); }
+__device__ __forceinline__ float4 load4(const __nv_bfloat16 *p)
+{
+    const uint2 u = *reinterpret_cast<const uint2 *>(p);
+    return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u),
+                       __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xffff0000u));
+}
+
 // Descriptors (low words): K step kk of a K-major tile in panels of 64 elements, and of an MN-major
 // [token][channel] tile in panels of 64 channels; `base` the tile's own.
 __device__ __forceinline__ uint32_t k_tile(uint32_t saddr) { return desc_sw128_lo(saddr, 16); }
