@@ -296,6 +296,13 @@ def test_empty_calls(kda):
         assert dg.shape == (2, 0, 2) and torch.equal(ds0, x["dsf"])
         g = torch.zeros(2, device="cuda") - 0.1
         assert (kda.kda_linattn_chunk_bwd(x["q"], x["k"], x["v"], g, x["do"], x["dsf"])[3] == 0).all()
+        cu = torch.zeros(4, dtype=torch.int32, device="cuda")   # three empty documents
+        x = dev(make(9, dtype, 1, 0, 1, 2, 64, 64, init=True))
+        s0 = torch.randn(3, 2, 64, 64, device="cuda")
+        o, sf = kda.kda_linattn_chunk_fwd(x["q"], x["k"], x["v"], x["g"], cu_seqlens=cu, initial_state=s0)
+        assert o.shape == (1, 0, 2, 64) and torch.equal(sf, s0)
+        ds0 = kda.kda_linattn_chunk_bwd(x["q"], x["k"], x["v"], x["g"], x["do"], s0, cu_seqlens=cu, initial_state=s0)[4]
+        assert torch.equal(ds0, s0)
 
 
 @gpu
