@@ -803,7 +803,9 @@ cudaError_t launch_kernel(const LinChunkParams &p, cudaStream_t st)
     const cudaError_t e = opt_in(lin_chunk_kernel<DX, DZ, STATE, OUT32>, SM_ALLOC, done);
     if (e != cudaSuccess) return e;
     const LinRun &r = p.a[0];
-    const unsigned units = (unsigned)(r.seg_chunks ? r.slots : r.num_seqs);
+    // in turn, sequences of one length have as many segments each; packed ones have no more than there are slots
+    const int each = r.tickets && !r.cu_seqlens ? std::max(1, (r.T + r.seg_tokens - 1) / r.seg_tokens) : 0;
+    const unsigned units = (unsigned)(each ? r.num_seqs * each : r.seg_chunks ? r.slots : r.num_seqs);
     lin_chunk_kernel<DX, DZ, STATE, OUT32><<<units * r.H * p.passes, NT, SM_ALLOC, st>>>(p);
     return cudaGetLastError();
 }
