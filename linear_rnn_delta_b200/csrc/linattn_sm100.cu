@@ -67,12 +67,15 @@ struct GateStage {
     short from[128];    // ... of channel j, first (backward: last) token
 };
 constexpr uint32_t SM_BAR = SM_GATE + NS * sizeof(GateStage);
-enum { B_FULL = 0, B_EMPTY = NS, B_QKF = 2 * NS, B_QKE, B_PZ, B_OF = B_PZ + 2, B_KB = B_OF + 2,
+enum { B_FULL = 0, B_EMPTY = NS, B_QKF = 2 * NS, B_QKE = B_QKF + NS, B_PZ, B_OF = B_PZ + 2, B_KB = B_OF + 2,
        B_KVF, B_S, B_SE, B_DRAIN, NBAR = B_DRAIN + 3 };
 // full: a stage's tiles and decays; empty: it may be loaded again; QKF, KVF, SE, OF: QK, KV, the state's product,
 // O are complete; QKE: QK is read; and what an MMA needs, all of it on one barrier (a wait costs the issuing
 // warp some 200 cycles even when it is over): PZ: P and Z^T for Z^T P^T; KB: Z^T's parts, and KV read, for KV;
-// S: the state's parts, and O read, for the state's product
+// S: the state's parts, and O read, for the state's product.
+// A wait for a phase by its parity needs that the phase after it cannot end first.  Whoever waits is among those who
+// let that one begin, but for QKF: warps 4-11 wait for it in some chunks only, and QK_{i+2} needs nothing later from
+// them than PZ_{i-1}.  It has a barrier for each load stage (QK_{i+4} needs PZ_{i+1}).
 constexpr uint32_t SM_MISC = SM_BAR + NBAR * 8;       // tensor-memory address, abort flag
 constexpr uint32_t SM_ALLOC = SM_MISC + 16 + 1024;
 static_assert(SM_ALLOC <= 232448, "shared memory budget");
@@ -152,7 +155,7 @@ __global__ void __launch_bounds__(NT, 1) lin_chunk_kernel(const __grid_constant_
             mbar_init(bar + B_FULL + s, 2);   // the loads' bytes, the decays
             mbar_init(bar + B_EMPTY + s, STATE ? 1 + 2 * JW : 2 + 2 * JW + 4);   // products, state, outputs
         }
-        mbar_init(bar + B_QKF, 1);
+        for (int s = 0; s < NS; ++s) mbar_init(bar + B_QKF + s, 1);
         mbar_init(bar + B_QKE, 2);
         for (int s = 0; s < 2; ++s) {
             mbar_init(bar + B_PZ + s, 2 + 8);
@@ -182,7 +185,7 @@ __global__ void __launch_bounds__(NT, 1) lin_chunk_kernel(const __grid_constant_
                 const int s = i % NS, pb = i & 1;
                 const GateStage &G = gates[s];
                 // P's buffer is free once O_{i-2} has read it
-                if (!wait(bar + B_FULL + s, (i / NS) & 1, s_abort) || !wait(bar + B_QKF, i & 1, s_abort) ||
+                if (!wait(bar + B_FULL + s, (i / NS) & 1, s_abort) || !wait(bar + B_QKF + s, (i / NS) & 1, s_abort) ||
                     (i >= 2 && !wait(bar + B_OF + pb, ((i >> 1) - 1) & 1, s_abort)))
                     break;
                 tc_fence_after();
@@ -375,7 +378,7 @@ __global__ void __launch_bounds__(NT, 1) lin_chunk_kernel(const __grid_constant_
             }
             if (!ok) break;
             if (!STATE && !G.narrow) {   // w_r goes to X, which QK_i has read
-                ok = ok && wait(bar + B_QKF, i & 1, s_abort);
+                ok = ok && wait(bar + B_QKF + s, (i / NS) & 1, s_abort);
 #pragma unroll 1
                 for (int e = t; e < C * DX / 8; e += ZT) {
                     uint32_t *x = reinterpret_cast<uint32_t *>(st + e * 16);
@@ -693,7 +696,7 @@ __global__ void __launch_bounds__(NT, 1) lin_chunk_kernel(const __grid_constant_
 #pragma unroll 2
                 for (int k = 0; k < DX / 16; ++k)
                     mma_bf16_warp(tbase + TM_QK, dK(x, k), dK(y, k), ID_QK, k > 0, lead);
-                mma_commit_warp(bar + B_QKF, lead);
+                mma_commit_warp(bar + B_QKF + s, lead);
             }
         } else if (!STATE && warp == 26) {
             // ---- O_i: the state's product and the chunk's
