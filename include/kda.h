@@ -128,7 +128,13 @@ enum kda_status {
  * waiting for them after about 1 ms, so that the bounded-wait expiry runs on
  * demand.  That pair's o is left unwritten and its final state is NaN; every
  * other pair is computed normally; kda_device_status then reports
- * KDA_ERR_DEVICE_TIMEOUT with KDA_DEVICE_WAIT_TIMEOUT.  Nothing faults. */
+ * KDA_ERR_DEVICE_TIMEOUT with KDA_DEVICE_WAIT_TIMEOUT.  Nothing faults.
+ * Linear attention: kda_linattn_chunk_fwd takes it where it walks segments in
+ * turn (the first segment of (sequence 0, head 0) does not hand its state
+ * over, the second gives up waiting for it: its o is left unwritten, what
+ * follows it of that pair is NaN), kda_linattn_chunk_bwd in the tensor-core
+ * form (dg of the first 64 tokens and head 0 gives up waiting for its inputs:
+ * NaN). */
 #define KDA_FLAG_DEBUG_STALL   64u
 
 /* Bits of the device failure word (kda_device_status). */
@@ -366,8 +372,12 @@ int kda_decode_step(int variant, int gate_range, int dtype,
  * kda_chunk_fwd_ws (chunk_states: the state after every 64 tokens of a
  * sequence and after its last one, at the chunk slots described there).
  * Sizes: B >= 1, T >= 0, d_k and d_v in {16, 32, 64, 128}, B*T < 2^30.
- * Flags: KDA_FLAG_VALIDATE_RANGE (g and cu_seqlens; waits for the outcome) and
- * KDA_FLAG_FORCE_SCAN (token-by-token kernel).  o does not depend on tokens
+ * Flags: KDA_FLAG_VALIDATE_RANGE (g and cu_seqlens; waits for the outcome),
+ * KDA_FLAG_FORCE_SCAN (token-by-token kernel) and KDA_FLAG_DEBUG_STALL.  After
+ * KDA_DEVICE_WAIT_TIMEOUT (kda_device_status) the final state of the affected
+ * (sequence, head) is NaN and its o and chunk_states are undefined, as are the
+ * gradients of a backward call, except for dg of a chunk whose own wait ran
+ * out, which is NaN.  o does not depend on tokens
  * behind it nor on other sequences of the batch, whatever their values.
  */
 
@@ -398,7 +408,8 @@ int kda_linattn_chunk_fwd(int dtype, int B, int T, int Hk, int H, int d_k, int d
  *   dg_t = sum_{r >= t} (q_r . dq_r - k_r . dk_r) + <S_T, dL/dS_T>.
  * At g_t = -infinity dg_t is 0, the slope of e^g there.  Deterministic.  No
  * output may share memory with an input.  workspace as above,
- * kda_linattn_chunk_bwd_workspace_size bytes.  Flags: KDA_FLAG_FORCE_SCAN.
+ * kda_linattn_chunk_bwd_workspace_size bytes.  Flags: KDA_FLAG_FORCE_SCAN,
+ * KDA_FLAG_DEBUG_STALL.
  */
 size_t kda_linattn_chunk_bwd_workspace_size(int dtype, int B, int T, int Hk, int H, int d_k, int d_v,
                                             int has_cu_seqlens, int num_seqs);

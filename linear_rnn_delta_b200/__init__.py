@@ -38,7 +38,7 @@ FLAG_FORCE_FUSED = 4   # tensor-core path, single fused kernel
 FLAG_FORCE_SPLIT = 8   # tensor-core path, preparation kernel + chain kernel
 FLAG_GATE_LOGITS = 16  # alpha and gates given as logits; the kernels apply the activations
 FLAG_L2NORM_K = 32     # k given unnormalised; the kernels L2-normalise it per token and head
-FLAG_DEBUG_STALL = 64  # testing aid (with FLAG_FORCE_SPLIT): one chain CTA's first wait runs out
+FLAG_DEBUG_STALL = 64  # testing aid (with FLAG_FORCE_SPLIT, or in linear attention): one CTA's wait runs out
 DEVICE_WAIT_TIMEOUT = 1   # kda_device_status bits
 DEVICE_SLOT_MISSING = 2
 DEVICE_BAD_INDEX = 4      # a state-cache row or slot index was too large

@@ -40,6 +40,7 @@ struct LinRun {
     // segments in turn (tensor-core form): tickets given out [H] and state hand-overs done [slot][H], zero at the
     // launch; NULL: side by side
     int *tickets, *handed;
+    int stall;                  // testing aid: (sequence 0, head 0)'s first segment in turn does not hand its state over
 };
 
 // Up to three passes of one shape, one cut of the token axis and one output type, side by side.
@@ -66,6 +67,7 @@ struct LinGateGrad {
     long long rows;
     int Hk, H, dk, dv, num_seqs, T, slots;
     const int32_t *cu_seqlens;
+    int stall;                      // testing aid (chunk form): slot 0 of head 0 does not load its tiles
 };
 
 cudaError_t launch_lin_scan(const LinRuns &r, int passes, int dx, int dz, bool bf16, cudaStream_t st);

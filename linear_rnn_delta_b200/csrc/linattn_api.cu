@@ -187,7 +187,7 @@ extern "C" int kda_linattn_chunk_fwd(int dtype, int B, int T, int Hk, int H, int
 {
     LinSizes s;
     CHECK(lin_sizes(s, dtype, B, T, Hk, H, d_k, d_v, cu_seqlens != nullptr, num_seqs));
-    if (flags & ~(KDA_FLAG_VALIDATE_RANGE | KDA_FLAG_FORCE_SCAN))
+    if (flags & ~(KDA_FLAG_VALIDATE_RANGE | KDA_FLAG_FORCE_SCAN | KDA_FLAG_DEBUG_STALL))
         return fail(KDA_ERR_INVALID_ARG, "kda_linattn_chunk_fwd: unknown or unsupported flag bits 0x%x", flags);
     if (T > 0) {
         CHECK(need_ptr(q, "q"));
@@ -201,10 +201,12 @@ extern "C" int kda_linattn_chunk_fwd(int dtype, int B, int T, int Hk, int H, int
     CHECK(opt_ptr(final_state, "final_state"));
     CHECK(opt_ptr(chunk_states, "chunk_states"));
     CHECK(opt_ptr(workspace, "workspace"));
-    const size_t need = kda_linattn_chunk_fwd_workspace_size(dtype, B, T, Hk, H, d_k, d_v, cu_seqlens != nullptr,
-                                                             num_seqs, flags);
-    if (need && (!workspace || workspace_bytes < need))
-        return fail(KDA_ERR_INVALID_ARG, "kda_linattn_chunk_fwd needs a workspace of %zu bytes", need);
+    const bool chunk = chunk_form(s, flags);
+    const Segments segs = segments(s, 1, chunk);
+    if ((flags & KDA_FLAG_DEBUG_STALL) && !segs.turns)
+        return fail(KDA_ERR_INVALID_ARG, "KDA_FLAG_DEBUG_STALL needs segments in turn");
+    if (segs.bytes && (!workspace || workspace_bytes < segs.bytes))
+        return fail(KDA_ERR_INVALID_ARG, "kda_linattn_chunk_fwd needs a workspace of %zu bytes", segs.bytes);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (flags & KDA_FLAG_VALIDATE_RANGE) {
         int bad_g = 0, bad_cu = 0;
@@ -226,8 +228,8 @@ extern "C" int kda_linattn_chunk_fwd(int dtype, int B, int T, int Hk, int H, int
     r.snap = chunk_states;
     r.snap_tokens = kda::SLOT_TOKENS;
     r.out = o;
-    const bool chunk = chunk_form(s, flags);
-    const cudaError_t e = launch_runs(&r, 1, d_k, d_v, chunk, dtype == KDA_DTYPE_BF16, segments(s, 1, chunk),
+    r.stall = (flags & KDA_FLAG_DEBUG_STALL) != 0;
+    const cudaError_t e = launch_runs(&r, 1, d_k, d_v, chunk, dtype == KDA_DTYPE_BF16, segs,
                                       static_cast<uint8_t *>(workspace), st);
     if (e != cudaSuccess) return cuda_fail(e, "kda_linattn_chunk_fwd launch");
     return KDA_OK;
@@ -252,8 +254,10 @@ extern "C" int kda_linattn_chunk_bwd(int dtype, int B, int T, int Hk, int H, int
 {
     LinSizes s;
     CHECK(lin_sizes(s, dtype, B, T, Hk, H, d_k, d_v, cu_seqlens != nullptr, num_seqs));
-    if (flags & ~KDA_FLAG_FORCE_SCAN)
+    if (flags & ~(KDA_FLAG_FORCE_SCAN | KDA_FLAG_DEBUG_STALL))
         return fail(KDA_ERR_INVALID_ARG, "kda_linattn_chunk_bwd: unknown or unsupported flag bits 0x%x", flags);
+    if ((flags & KDA_FLAG_DEBUG_STALL) && !chunk_form(s, flags))
+        return fail(KDA_ERR_INVALID_ARG, "KDA_FLAG_DEBUG_STALL needs the tensor-core form");
     if (T > 0) {
         const void *ptrs[] = {q, k, v, d_o, dq, dk, dv};
         const char *names[] = {"q", "k", "v", "d_o", "dq", "dk", "dv"};
@@ -329,6 +333,7 @@ extern "C" int kda_linattn_chunk_bwd(int dtype, int B, int T, int Hk, int H, int
     gg.Hk = Hk; gg.H = H; gg.dk = d_k; gg.dv = d_v;
     gg.num_seqs = s.N; gg.T = T; gg.slots = L.slots;
     gg.cu_seqlens = cu_seqlens;
+    gg.stall = (flags & KDA_FLAG_DEBUG_STALL) != 0;
     if ((e = kda::launch_lin_gate_grad(gg, bf16, chunk, st)) != cudaSuccess) return cuda_fail(e, "kda_linattn_chunk_bwd dg");
     return KDA_OK;
 }

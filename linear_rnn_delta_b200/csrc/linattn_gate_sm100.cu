@@ -77,21 +77,24 @@ __global__ void __launch_bounds__(NT, 2) lin_gate_kernel(const __grid_constant__
         if (st1) asm volatile("prefetch.global.L2 [%0];" :: "l"(st1 + e * 32));
     }
 
+    const bool stall = a.stall && blockIdx.x == 0;
     if (warp == 0) tmem_alloc(&s_tmem, TM_COLS);
     if (tid == 0) {
         mbar_init(s_bar, 1);
         mbar_init(s_bar + 1, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-        mbar_expect_tx(s_bar, (DK + DV) * 2 * C * 2);
+        if (!stall) {
+            mbar_expect_tx(s_bar, (DK + DV) * 2 * C * 2);
 #pragma unroll
-        for (int p = 0; p < DK / 64; ++p) {
-            tma_load_3d(sm + p * 8192, &P.q, s_bar, p * 64, hk, (int)row);
-            tma_load_3d(sm + TILE + p * 8192, &P.k, s_bar, p * 64, hk, (int)row);
-        }
+            for (int p = 0; p < DK / 64; ++p) {
+                tma_load_3d(sm + p * 8192, &P.q, s_bar, p * 64, hk, (int)row);
+                tma_load_3d(sm + TILE + p * 8192, &P.k, s_bar, p * 64, hk, (int)row);
+            }
 #pragma unroll
-        for (int p = 0; p < DV / 64; ++p) {
-            tma_load_3d(sm + 2 * TILE + p * 8192, &P.d_o, s_bar, p * 64, h, (int)row);
-            tma_load_3d(sm + 3 * TILE + p * 8192, &P.v, s_bar, p * 64, h, (int)row);
+            for (int p = 0; p < DV / 64; ++p) {
+                tma_load_3d(sm + 2 * TILE + p * 8192, &P.d_o, s_bar, p * 64, h, (int)row);
+                tma_load_3d(sm + 3 * TILE + p * 8192, &P.v, s_bar, p * 64, h, (int)row);
+            }
         }
     }
     if (warp == 1) {   // sums of log2-decays
@@ -118,14 +121,14 @@ __global__ void __launch_bounds__(NT, 2) lin_gate_kernel(const __grid_constant__
     __syncthreads();
     tc_fence_after();
     const uint32_t tbase = s_tmem, tlane = tbase + ((uint32_t)(quarter * 32) << 16);
-    bool ok = mbar_wait_cycles(s_bar, 0, WAIT_LIMIT);
+    bool ok = mbar_wait_cycles(s_bar, 0, stall ? STALL_LIMIT : WAIT_LIMIT);
     ok = __syncthreads_and(ok) != 0;
-    uint32_t phase = 0;
+    uint32_t products = 0;   // of which all but the last are complete
     // products are issued by warp 0, everybody waits for them
     auto finish = [&]() {
         if (warp == 0) mma_commit_warp(s_bar + 1, lane == 0);
-        ok = __syncthreads_and(mbar_wait_cycles(s_bar + 1, phase, WAIT_LIMIT)) != 0 && ok;
-        phase ^= 1;
+        ok = __syncthreads_and(mbar_wait_cycles(s_bar + 1, products & 1, WAIT_LIMIT)) != 0 && ok;
+        ++products;
         tc_fence_after();
     };
 
@@ -307,10 +310,14 @@ __global__ void __launch_bounds__(NT, 2) lin_gate_kernel(const __grid_constant__
             if (lane == 0) a.partial[(size_t)slot * a.H + h] = sum;
         }
     }
+    if (!ok && tid == 0) {   // what was started ends before the CTA does
+        atomicOr(P.status, DEV_WAIT_TIMEOUT);
+        if (!stall) mbar_wait_cycles(s_bar, 0, WAIT_LIMIT);
+        if (products) mbar_wait_cycles(s_bar + 1, (products - 1) & 1, WAIT_LIMIT);
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (!ok && tid == 0) atomicOr(P.status, DEV_WAIT_TIMEOUT);
     if (warp == 0) tmem_dealloc(tbase, TM_COLS);
 }
 

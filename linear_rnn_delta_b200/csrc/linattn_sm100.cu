@@ -94,7 +94,7 @@ __device__ __forceinline__ void hand_over(int *count)
 {
     asm volatile("red.release.gpu.global.add.s32 [%0], 1;" ::"l"(count) : "memory");
 }
-__device__ __forceinline__ bool wait_handed(const int *count, int all, volatile int *abort)
+__device__ __forceinline__ bool wait_handed(const int *count, int all, long long limit, volatile int *abort)
 {
     bool ok = true;
     if ((threadIdx.x & 31) == 0) {
@@ -103,7 +103,7 @@ __device__ __forceinline__ bool wait_handed(const int *count, int all, volatile 
             int v;
             asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(count) : "memory");
             if (v >= all) break;
-            if (*abort || clock64() - t0 > WAIT_LIMIT) {
+            if (*abort || clock64() - t0 > limit) {
                 *abort = 1;
                 ok = false;
                 break;
@@ -540,7 +540,10 @@ __global__ void __launch_bounds__(NT, 1) lin_chunk_kernel(const __grid_constant_
             float *s_out = STATE ? a.seg_state + woff : gives ? a.seg_state + to_slot * (DX * DZ)
                            : a.s_out && closing ? a.s_out + soff : nullptr;
             bool ok = true;
-            if (turns && given) ok = wait_handed(a.handed + (size_t)work.slot * a.H + h, 2 * JW, s_abort);
+            const bool stall = a.stall && n == 0 && h == 0;
+            if (turns && given)
+                ok = wait_handed(a.handed + (size_t)work.slot * a.H + h, 2 * JW,
+                                 stall && work.c0 == a.seg_chunks ? STALL_LIMIT : WAIT_LIMIT, s_abort);
             // between memory and the registers by way of the tensor memory that KV has later: short loops
             const uint32_t scratch = tlane + TM_KV + i0;
             {
@@ -638,7 +641,7 @@ __global__ void __launch_bounds__(NT, 1) lin_chunk_kernel(const __grid_constant_
             if (!ok && s_out)
 #pragma unroll 1
                 for (int e = 0; e < CX; ++e) s_out[(size_t)(i0 + e) * DZ + j] = __int_as_float(0x7fc00000);
-            if (gives) {
+            if (gives && !(stall && opening)) {
                 __syncwarp();
                 if (lane == 0) hand_over(a.handed + to_slot);
             }
@@ -720,8 +723,8 @@ __global__ void __launch_bounds__(NT, 1) lin_chunk_kernel(const __grid_constant_
                 mma_commit_warp(bar + B_EMPTY + i % NS, lead);
             }
         }
-        // products still running are waited for here (every product of a full run is, by its readers)
-        if (!ok && warp >= 25) {
+        // no product runs on: this warp may have issued all of its own and a reader have given up since
+        if (nch > 0 && (warp == 25 || (!STATE && warp > 25))) {
             mma_commit_warp(bar + B_DRAIN + warp - 25, lead);
             if (lane == 0) mbar_wait_cycles(bar + B_DRAIN + warp - 25, 0, WAIT_LIMIT);
         }

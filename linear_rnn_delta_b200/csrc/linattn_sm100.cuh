@@ -20,6 +20,7 @@ constexpr uint32_t STAGE = 3 * TILE;                  // X, Y, Z
 
 constexpr long long WAIT_LIMIT = 1ll << 32;           // cycles, about 2 s (the last waits of a CTA)
 constexpr uint32_t WAIT_NS = 1000000, WAIT_POLLS = 2000;   // a poll sleeps for up to 1 ms: about 2 s
+constexpr long long STALL_LIMIT = 1ll << 21;          // testing aid: about 1 ms
 constexpr unsigned DEV_WAIT_TIMEOUT = 1u;
 
 // What a CTA walks, in chunks of U tokens: chunks c0 .. c0 + nch - 1 of sequence n (nall in all; none: the slot is nobody's).

@@ -2,7 +2,9 @@
 long segments, waits that run out, gradients as autograd hands them over.
 
 Tolerances and helpers are test_linattn.py's."""
+import ctypes
 import math
+import time
 
 import pytest
 import torch
@@ -54,3 +56,71 @@ def test_reset_and_bad_value_in_one_chunk(kda, T, chunk, d, bad):
         if state is not None:
             assert torch.equal(state[0, 1], state0[0, 1]) and torch.isnan(state[0, 0]).all()
     assert kda.kda_device_status() == (0, 0)
+
+
+# ---- waits that run out --------------------------------------------------------------------------------------------
+
+STALLED = dict(B=3, T=4096, Hk=1, H=50, dk=64, dv=64)   # 50 heads of three sequences: four segments each, in turn
+
+
+def refusal(kda, s, flags, bwd=False, cu=False):
+    """Why a call without a workspace is refused (the pointers are never followed)."""
+    P = ctypes.c_void_p(0x10000)
+    sizes = [0, *s.values()]
+    N = cu or s["B"]
+    head = [*sizes, P, P, P, P, 1, P if cu else None, N, None]
+    if bwd:
+        rc = kda.lib.kda_linattn_chunk_bwd(*head, P, None, P, P, P, P, None, None, 0, flags, None)
+    else:
+        rc = kda.lib.kda_linattn_chunk_fwd(*head, None, None, P, None, 0, flags, None)
+    assert rc == 1
+    return kda.lib.kda_last_error_detail().decode()
+
+
+def test_stall_flag_needs_a_wait_to_stall(kda):
+    assert "workspace" in refusal(kda, STALLED, kda.FLAG_DEBUG_STALL)
+    for s, flags in ((dict(STALLED, B=1, H=1), 0), (dict(STALLED, B=1, H=1, T=8192), 0), (STALLED, kda.FLAG_FORCE_SCAN)):
+        assert "in turn" in refusal(kda, s, flags | kda.FLAG_DEBUG_STALL)
+    assert "workspace" in refusal(kda, STALLED, kda.FLAG_DEBUG_STALL, bwd=True)
+    assert "tensor-core" in refusal(kda, dict(STALLED, dk=32), kda.FLAG_DEBUG_STALL, bwd=True)
+    assert "tensor-core" in refusal(kda, STALLED, kda.FLAG_DEBUG_STALL | kda.FLAG_FORCE_SCAN, bwd=True)
+
+
+@gpu
+def test_hand_over_that_never_comes(kda):
+    """The segment that waits gives up, hands NaN on and ends; its successors end; nothing else notices."""
+    s = STALLED
+    x = dev(make(41, torch.bfloat16, s["B"], s["T"], s["Hk"], s["H"], s["dk"], s["dv"], init=True))
+    run = lambda flags=0: kda.kda_linattn_chunk_fwd(x["q"], x["k"], x["v"], x["g"], initial_state=x["s0"], flags=flags)  # noqa: E731
+    kda.kda_device_status()
+    want, sf = run()
+    assert kda.kda_device_status() == (0, 0)
+    t0 = time.time()
+    o, st = run(kda.FLAG_DEBUG_STALL)
+    assert kda.kda_device_status() == (5, kda.DEVICE_WAIT_TIMEOUT)
+    assert time.time() - t0 < 1.0   # no further wait ran out (each about 2 s)
+    assert torch.isnan(st[0, 0]).all() and torch.equal(st[0, 1:], sf[0, 1:]) and torch.equal(st[1:], sf[1:])
+    assert torch.equal(o[0, :, 1:], want[0, :, 1:]) and torch.equal(o[1:], want[1:])
+    # a segment has 16 or 17 chunks: the first is as it was, behind the second there is NaN
+    assert torch.equal(o[0, :1024, 0], want[0, :1024, 0]) and torch.isnan(o[0, 2176:, 0].float()).all()
+    o, st = run()
+    assert torch.equal(o, want) and torch.equal(st, sf) and kda.kda_device_status() == (0, 0)
+
+
+@gpu
+@pytest.mark.parametrize("d", [64, 128])
+def test_gate_gradient_whose_inputs_never_come(kda, d):
+    x = dev(make(42, torch.bfloat16, 2, 150, 1, 2, d, d, init=True))
+    run = lambda flags=0: kda.kda_linattn_chunk_bwd(x["q"], x["k"], x["v"], x["g"], x["do"], x["dsf"],  # noqa: E731
+                                                    initial_state=x["s0"], flags=flags)
+    kda.kda_device_status()
+    want = run()
+    assert kda.kda_device_status() == (0, 0)
+    t0 = time.time()
+    got = run(kda.FLAG_DEBUG_STALL)
+    assert kda.kda_device_status() == (5, kda.DEVICE_WAIT_TIMEOUT) and time.time() - t0 < 1.0
+    assert all(torch.equal(a, b) for i, (a, b) in enumerate(zip(got, want)) if i != 3)
+    dg, dg0 = got[3], want[3]
+    assert torch.isnan(dg[0, :64, 0]).all() and torch.equal(dg[0, 64:, 0], dg0[0, 64:, 0])
+    assert torch.equal(dg[0, :, 1], dg0[0, :, 1]) and torch.equal(dg[1], dg0[1])
+    assert all(torch.equal(a, b) for a, b in zip(run(), want)) and kda.kda_device_status() == (0, 0)
