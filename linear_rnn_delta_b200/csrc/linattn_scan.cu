@@ -159,7 +159,7 @@ __global__ void __launch_bounds__(LinScanShape<DX, DZ>::NTH) lin_scan_kernel(con
                     s_wide[buf] = wide;
                 }
                 if (STATE) {
-                    sum += f;
+                    sum = max(sum + f, lin::FIX_LEAST);
                     any_nan = any_nan || nan;
                 }
             }

@@ -298,7 +298,7 @@ __global__ void __launch_bounds__(NT, 1) lin_chunk_kernel(const __grid_constant_
                     G.w[t] = w;
                     G.u[t] = u;
                 }
-                if (STATE) sum += end, any_nan = any_nan || (nan_a | nan_b);
+                if (STATE) sum = max(sum + end, FIX_LEAST), any_nan = any_nan || (nan_a | nan_b);
                 narrow = __all_sync(0xffffffffu, narrow);
                 if (lane == 0) {
                     G.total = (nan_a | nan_b) ? nan : fix_exp2(end);

@@ -181,6 +181,9 @@ __device__ __forceinline__ long long fix_log2(float g)
     const float n = rintf(hi);
     return ((long long)(int)n << 32) + (long long)__float2int_rn(((hi - n) + lo) * 4294967296.f);
 }
+// Sums over a whole segment stop at 2^-256, whose decay is 0: resets count 2^-14427 each, and 150000 of them would
+// leave the 31 bits before the point.
+constexpr long long FIX_LEAST = -(256ll << 32);
 // integer part and rest in [-1/2, 1/2)
 __device__ __forceinline__ int fix_int(long long x) { return (int)((x + 0x80000000ll) >> 32); }
 __device__ __forceinline__ float fix_rest(long long x) { return (float)(int)(unsigned)x * 2.3283064365386963e-10f; }

@@ -4,6 +4,7 @@ long segments, waits that run out, gradients as autograd hands them over.
 Tolerances and helpers are test_linattn.py's."""
 import ctypes
 import math
+import re
 import time
 
 import pytest
@@ -124,3 +125,56 @@ def test_gate_gradient_whose_inputs_never_come(kda, d):
     assert torch.isnan(dg[0, :64, 0]).all() and torch.equal(dg[0, 64:, 0], dg0[0, 64:, 0])
     assert torch.equal(dg[0, :, 1], dg0[0, :, 1]) and torch.equal(dg[1], dg0[1])
     assert all(torch.equal(a, b) for a, b in zip(run(), want)) and kda.kda_device_status() == (0, 0)
+
+
+# ---- long segments -------------------------------------------------------------------------------------------------
+
+RESETS = [  # T, H, d; d = 16 takes the token scan.  Segments of more than 148860 tokens
+    (450000, 47, 64),
+    (600000, 150, 16),
+]
+
+
+@pytest.mark.parametrize("T,H,d", RESETS)
+def test_segments_are_long(kda, T, H, d):
+    need = int(re.search(r"(\d+) bytes", refusal(kda, dict(B=1, T=T, Hk=1, H=H, dk=d, dv=d), 0)).group(1))
+    assert "in turn" in refusal(kda, dict(B=1, T=T, Hk=1, H=H, dk=d, dv=d), kda.FLAG_DEBUG_STALL)
+    slots = need // (H * d * d * 4)   # a state each, and one of the sequence: not cut into more than slots - 1
+    assert 148860 * (slots - 1) < T
+
+
+def small_ints(*shape, seed):
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    return torch.randint(-1, 2, shape, generator=gen, device="cuda", dtype=torch.int8).to(torch.bfloat16)
+
+
+@gpu
+@pytest.mark.parametrize("T,H,d", RESETS)
+def test_resets_all_along_a_long_segment(kda, T, H, d):
+    """Every token resets: o_t = (q_t . k_t) v_t, in small whole numbers, which every format here holds."""
+    q, k, v = small_ints(1, T, 1, d, seed=1), small_ints(1, T, 1, d, seed=2), small_ints(1, T, H, d, seed=3)
+    g = torch.full((H,), -math.inf, device="cuda")
+    o, sf = kda.kda_linattn_chunk_fwd(q, k, v, g, initial_state=torch.ones(1, H, d, d, device="cuda"))
+    for t in range(0, T, 1 << 15):
+        part = slice(t, t + (1 << 15))
+        want = (q[:, part].float() * k[:, part].float()).sum(-1, keepdim=True) * v[:, part].float()
+        assert torch.equal(o[:, part].float(), want), t
+    assert torch.equal(sf[0], k[0, -1].float()[:, :, None] * v[0, -1].float()[:, None, :])
+
+
+@gpu
+def test_resets_all_along_a_long_segment_backward(kda):
+    """dv_t = (q_t . k_t) do_t, dq_t the sum over the heads of (do_t . v_t) k_t, rounded once."""
+    T, H, d = 600000, 75, 16   # two passes of a launch: cut like 150 heads
+    q, k = small_ints(1, T, 1, d, seed=1), small_ints(1, T, 1, d, seed=2)
+    v, do = small_ints(1, T, H, d, seed=3), small_ints(1, T, H, d, seed=4)
+    g = torch.full((H,), -math.inf, device="cuda")
+    dq, dk, dv, dg, _ = kda.kda_linattn_chunk_bwd(q, k, v, g, do)
+    for t in range(0, T, 1 << 15):
+        part = slice(t, t + (1 << 15))
+        qk = (q[:, part].float() * k[:, part].float()).sum(-1, keepdim=True)
+        dov = (do[:, part].float() * v[:, part].float()).sum((-1, -2))[..., None, None]
+        assert torch.equal(dv[:, part].float(), qk * do[:, part].float()), t
+        assert torch.equal(dq[:, part], (dov * k[:, part].float()).to(torch.bfloat16)), t
+        assert torch.equal(dk[:, part], (dov * q[:, part].float()).to(torch.bfloat16)), t
+    assert (dg == 0).all()
