@@ -372,6 +372,10 @@ int kda_decode_step(int variant, int gate_range, int dtype,
  * kda_chunk_fwd_ws (chunk_states: the state after every 64 tokens of a
  * sequence and after its last one, at the chunk slots described there).
  * Sizes: B >= 1, T >= 0, d_k and d_v in {16, 32, 64, 128}, B*T < 2^30.
+ * Values: finite results need sums of (q_r . k_s) v_s and S^T q below 2^60 in
+ * magnitude (in the backward, of the products that take their places); in the
+ * tensor-core form (bf16, head sizes 64 and 128) what of them is below 2^-90
+ * may be lost.
  * Flags: KDA_FLAG_VALIDATE_RANGE (g and cu_seqlens; waits for the outcome),
  * KDA_FLAG_FORCE_SCAN (token-by-token kernel) and KDA_FLAG_DEBUG_STALL.  After
  * KDA_DEVICE_WAIT_TIMEOUT (kda_device_status) the final state of the affected

@@ -16,6 +16,9 @@
 // and out_r = w_r O_r: with the weights divided by w_r the two products share one accumulator.  L_rs / w_r
 // is e^{-c_s}, which stays in range while the chunk's decays multiply to no less than 2^-96 (`narrow`).  A chunk
 // that decays further (a reset, say) has P_rs = L_rs (x_r . y_s), out_r = O_r, and w_r goes to X, rounded.
+// Both kinds keep O and P 2^32 times smaller (exactly: a shift of exponents, taken back with w_r): e^{-c_s} (x_r . y_s) z_s
+// may be 2^96 times the output's own term, and unshifted it overflowed where that term was no more than 2^32.  Sums up
+// to 2^64 have room now, and what is lost at the other end lies below 2^-94.
 // All A operands but QK's are in tensor memory: the tensor core reads 128 bytes of shared memory a cycle,
 // and with A from there, too, operands alone would keep it busy for 1600 cycles a chunk and everybody
 // else's shared-memory accesses waiting.  Z^T gets there from Z by transposing matrix loads.
@@ -57,8 +60,8 @@ constexpr uint32_t SM_P = NS * STAGE;                 // P, two chunks' [64][64]
 constexpr uint32_t SM_GATE = SM_P + 2 * 8192;
 struct GateStage {
     float2 c[C];        // running sums of log2-decays, two floats
-    float b[C];         // L_rs / w_r
-    float w[C];         // w_r
+    float b[C];         // 2^-SHIFT L_rs / w_r
+    float w[C];         // 2^SHIFT w_r
     float u[C];         // u_s
     float total;        // e^{c_C}
     int nv;             // tokens of the chunk
@@ -80,7 +83,9 @@ constexpr uint32_t SM_MISC = SM_BAR + NBAR * 8;       // tensor-memory address, 
 constexpr uint32_t SM_ALLOC = SM_MISC + 16 + 1024;
 static_assert(SM_ALLOC <= 232448, "shared memory budget");
 
-constexpr long long NARROW = 96ll << 32;   // leaves x . y 31 binary orders before e^{-c_s} (x . y) overflows
+constexpr long long NARROW = 96ll << 32;
+constexpr int SHIFT = 32;                  // O and P are 2^-SHIFT times what they stand for
+constexpr float DOWN = 1.f / 4294967296.f, UP = 4294967296.f;
 
 // registers of the seven warpgroups: what they give up or take adds up to the launch's 72 each
 constexpr int RG_P = 72 /* the launch's own */, RG_Z = 64, RG_OUT = 56, RG_STATE = 104, RG_MMA = 40;
@@ -223,7 +228,7 @@ __global__ void __launch_bounds__(NT, 1) lin_chunk_kernel(const __grid_constant_
                             *reinterpret_cast<uint4 *>(prow + (((half * 4 + q) ^ (r & 7)) << 4)) =
                                 make_uint4(pk[4 * q], pk[4 * q + 1], pk[4 * q + 2], pk[4 * q + 3]);
                     } else {   // a strong decay or a reset in the chunk: each pair's own exponential
-                        const float2 cr = G.c[r];
+                        const float2 cr = make_float2(G.c[r].x + (rev ? SHIFT : -SHIFT), G.c[r].y);
 #pragma unroll 1
                         for (int q = 0; q < 4; ++q, keep >>= 8) {
                             float v[8];
@@ -284,9 +289,9 @@ __global__ void __launch_bounds__(NT, 1) lin_chunk_kernel(const __grid_constant_
                     const int t = 2 * lane + e;
                     const long long c = e ? run : run - fb, left = end - c;
                     float2 cc = make_float2((float)fix_int(c), fix_rest(c));
-                    float w = fix_exp2(rev ? left : c), u = fix_exp2(rev ? c : left);
+                    float w = fix_exp2((rev ? left : c) + ((long long)SHIFT << 32)), u = fix_exp2(rev ? c : left);
                     narrow = narrow && c < NARROW && -c < NARROW && left < NARROW && -left < NARROW;
-                    G.b[t] = fix_exp2(rev ? -left : -c);
+                    G.b[t] = fix_exp2((rev ? -left : -c) - ((long long)SHIFT << 32));
                     if (nan_a | nan_b) {   // a NaN decay is part of every sum from its token on
                         const unsigned upto = 0xffffffffu >> (31 - lane);
                         const bool seen = (nan_a & upto) || (nan_b & (e ? upto : upto >> 1));
@@ -382,7 +387,7 @@ __global__ void __launch_bounds__(NT, 1) lin_chunk_kernel(const __grid_constant_
 #pragma unroll 1
                 for (int e = t; e < C * DX / 8; e += ZT) {
                     uint32_t *x = reinterpret_cast<uint32_t *>(st + e * 16);
-                    const float w = G.w[(e & 511) >> 3];
+                    const float w = G.w[(e & 511) >> 3] * DOWN;
 #pragma unroll
                     for (int y = 0; y < 4; ++y) {
                         const float2 v = __fmul2_rn(unpack(x[y]), make_float2(w, w));
@@ -466,13 +471,12 @@ __global__ void __launch_bounds__(NT, 1) lin_chunk_kernel(const __grid_constant_
                         tc_fence_before();
                         warp_arrive(bar + B_S);
                     }
-                    if (narrow) {
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const float2 w = *reinterpret_cast<const float2 *>(&G.w[half * 32 + k * 8 + 2 * (lane & 3)]);
-                            v[2 * k] = __fmul2_rn(v[2 * k], w);
-                            v[2 * k + 1] = __fmul2_rn(v[2 * k + 1], w);
-                        }
+                    for (int k = 0; k < 4; ++k) {
+                        float2 w = make_float2(UP, UP);
+                        if (narrow) w = *reinterpret_cast<const float2 *>(&G.w[half * 32 + k * 8 + 2 * (lane & 3)]);
+                        v[2 * k] = __fmul2_rn(v[2 * k], w);
+                        v[2 * k + 1] = __fmul2_rn(v[2 * k + 1], w);
                     }
                     if (bad) {
 #pragma unroll
@@ -606,7 +610,7 @@ __global__ void __launch_bounds__(NT, 1) lin_chunk_kernel(const __grid_constant_
                         uint32_t hi[8], lo[8];
 #pragma unroll
                         for (int e = 0; e < 8; ++e) {
-                            float2 x = S[b * 8 + e];
+                            float2 x = __fmul2_rn(S[b * 8 + e], make_float2(DOWN, DOWN));
                             hi[e] = take_part(x);
                             lo[e] = pack_bf16(x.x, x.y);
                         }

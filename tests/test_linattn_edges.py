@@ -10,7 +10,7 @@ import time
 import pytest
 import torch
 
-from test_linattn import dev, make
+from test_linattn import DT, check_bwd, check_fwd, dev, make
 
 gpu = pytest.mark.gpu
 
@@ -178,3 +178,20 @@ def test_resets_all_along_a_long_segment_backward(kda):
         assert torch.equal(dq[:, part], (dov * k[:, part].float()).to(torch.bfloat16)), t
         assert torch.equal(dk[:, part], (dov * q[:, part].float()).to(torch.bfloat16)), t
     assert (dg == 0).all()
+
+
+# ---- large and small values ----------------------------------------------------------------------------------------
+
+@gpu
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("bf16", 64), ("bf16", 32), ("fp32", 64)])
+@pytest.mark.parametrize("size", [-24, 8, 12, 16])
+@pytest.mark.parametrize("decay", ["limit", "little", "strong"])
+def test_large_and_small_values(kda, dtype, d, size, decay):
+    """Inputs of 2^size; chunks that decay by nearly the 2^-96 up to which the weights are divided by the decay to
+    their token, hardly, or further."""
+    x = make(43, DT[dtype], 1, 150, 1, 2, d, d, init=True)
+    for n in ("q", "k", "v", "do", "s0", "dsf"):
+        x[n] = x[n] * 2.0 ** size
+    x["g"] = torch.full_like(x["g"], {"limit": -95.9 / 64 * math.log(2), "little": -0.01, "strong": -3.0}[decay])
+    check_fwd(kda, x, strong=decay == "strong")
+    check_bwd(kda, x, strong=decay == "strong")
