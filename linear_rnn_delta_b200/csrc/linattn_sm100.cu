@@ -116,7 +116,9 @@ __device__ __forceinline__ bool wait_handed(const int *count, int all, long long
             __nanosleep(200);
         }
     }
-    return __all_sync(0xffffffffu, ok);
+    ok = __all_sync(0xffffffffu, ok);
+    __syncwarp();   // passes lane 0's acquire on to the lanes that read the state (a vote does not)
+    return ok;
 }
 
 // Up to three passes of one shape; CTAs of a unit's passes and heads are neighbours
