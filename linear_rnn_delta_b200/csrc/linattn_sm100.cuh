@@ -173,13 +173,15 @@ __device__ __forceinline__ float ex2(float x)
     return y;
 }
 // Log2-decays are summed as 64-bit fixed point with 32 bits behind the point: sums and differences are exact,
-// a term is off by 2^-33.
+// a term is off by less than 3 2^-33.
 __device__ __forceinline__ long long fix_log2(float g)
 {
     // g log2(e) as two floats: the rounding of the product, and of log2(e), would show in long sums
     const float hi = g * 1.44269502f, lo = fmaf(g, 1.44269502f, -hi) + g * 1.92596303e-8f;
     const float n = rintf(hi);
-    return ((long long)(int)n << 32) + (long long)__float2int_rn(((hi - n) + lo) * 4294967296.f);
+    // hi - n and lo each on its own: their sum would be rounded to 24 bits (2^-26 off, the same for every token of a
+    // steady decay)
+    return ((long long)(int)n << 32) + __float2int_rn((hi - n) * 4294967296.f) + __float2int_rn(lo * 4294967296.f);
 }
 // Sums over a whole segment stop at 2^-256, whose decay is 0: resets count 2^-14427 each, and 150000 of them would
 // leave the 31 bits before the point.

@@ -195,3 +195,22 @@ def test_large_and_small_values(kda, dtype, d, size, decay):
     x["g"] = torch.full_like(x["g"], {"limit": -95.9 / 64 * math.log(2), "little": -0.01, "strong": -3.0}[decay])
     check_fwd(kda, x, strong=decay == "strong")
     check_bwd(kda, x, strong=decay == "strong")
+
+
+# ---- steady decays -------------------------------------------------------------------------------------------------
+
+@gpu
+def test_steady_decay_over_a_chunk(kda):
+    """A state that decays alone for 64 tokens.  The sum of their logarithms is off by less than 64 * 3 * 2^-33, the
+    exponential by two units (2^-22), the product by half of one: at a token's 2^-26, the last place of a logarithm in
+    fp32, the first would be 6.6e-7."""
+    decays = [-0.9012105464935303, -0.9419410228729248, -0.8910042643547058, -0.9726753234863281,
+              -0.9623535871505737, -0.870476245880127, -1.0030840635299683, -0.9521473050117493]
+    g = torch.tensor(decays, device="cuda")
+    x = torch.zeros(1, 64, 1, 64, device="cuda", dtype=torch.bfloat16)
+    v = torch.zeros(1, 64, 8, 64, device="cuda", dtype=torch.bfloat16)
+    s0 = 1 + torch.rand(1, 8, 64, 64, generator=torch.Generator(device="cuda").manual_seed(0), device="cuda")
+    _, sf = kda.kda_linattn_chunk_fwd(x, x, v, g, initial_state=s0)
+    want = s0.double() * torch.exp(64 * g.double())[:, None, None]
+    bound = 64 * 3 * 2.0 ** -33 * math.log(2) + 2.0 ** -22 + 2.0 ** -24
+    assert ((sf.double() / want - 1).abs() <= bound).all()
