@@ -656,6 +656,13 @@ def kda_linattn_chunk_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: 
     return dqt, dkt, dvt, dgt, ds0
 
 
+def _incoming(t: torch.Tensor, dtype):
+    """A gradient as autograd hands it over, as the kernels take it: of their dtype, contiguous, and 16-byte aligned,
+    which a part of another tensor's gradient (of torch.cat, say) need not be."""
+    t = t.to(dtype).contiguous()
+    return t.clone() if t.data_ptr() & 15 else t
+
+
 class KdaLinAttnFunction(torch.autograd.Function):
     """Differentiable forward: ``KdaLinAttnFunction.apply(q, k, v, g,
     cu_seqlens, initial_state)`` returns (o, final_state) from
@@ -673,9 +680,9 @@ class KdaLinAttnFunction(torch.autograd.Function):
     @torch.autograd.function.once_differentiable
     def backward(ctx, d_o, d_sf):
         q, k, v, g, cu_seqlens, initial_state = ctx.saved_tensors
-        d_o = torch.zeros_like(v) if d_o is None else d_o.to(q.dtype).contiguous()
+        d_o = torch.zeros_like(v) if d_o is None else _incoming(d_o, q.dtype)
         dq, dk, dv, dg, ds0 = kda_linattn_chunk_bwd(
-            q, k, v, g, d_o, None if d_sf is None else d_sf.float().contiguous(), cu_seqlens, initial_state,
+            q, k, v, g, d_o, None if d_sf is None else _incoming(d_sf, torch.float32), cu_seqlens, initial_state,
             d_initial_state=initial_state is not None and ctx.needs_input_grad[5])
         return dq, dk, dv, dg, None, ds0
 

@@ -214,3 +214,18 @@ def test_steady_decay_over_a_chunk(kda):
     want = s0.double() * torch.exp(64 * g.double())[:, None, None]
     bound = 64 * 3 * 2.0 ** -33 * math.log(2) + 2.0 ** -22 + 2.0 ** -24
     assert ((sf.double() / want - 1).abs() <= bound).all()
+
+
+# ---- autograd ------------------------------------------------------------------------------------------------------
+
+@gpu
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_gradients_that_are_parts_of_others(kda, dtype):
+    """The gradients of o and of the final state behind an odd number of other values: contiguous, not aligned."""
+    x = dev(make(44, DT[dtype], 1, 70, 1, 2, 64, 64, init=True))
+    want = kda.kda_linattn_chunk_bwd(x["q"], x["k"], x["v"], x["g"], x["do"], x["dsf"], initial_state=x["s0"])
+    leaves = [x[n].clone().requires_grad_() for n in ("q", "k", "v", "g", "s0")]
+    o, sf = kda.KdaLinAttnFunction.apply(*leaves[:4], None, leaves[4])
+    pad = lambda t: torch.cat([t.new_ones(1), t.flatten()])  # noqa: E731
+    got = torch.autograd.grad([pad(o), pad(sf)], leaves, [pad(x["do"]), pad(x["dsf"])])
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
