@@ -442,7 +442,8 @@ int kda_linattn_decode_step(int dtype, int N, int Hk, int H, int d_k, int d_v,
  * For a row x of d_v values with A = max |x|: scale = A / TOP, TOP = 127
  * (int8) or 448 (e4m3); code = the nearest to x TOP / A, ties to the even
  * code, decided as in exact arithmetic; the value read back is code * scale.
- * A row of zeros has scale 0.  A row that holds a NaN or an infinity has scale
+ * (int8, A = the largest finite value: the scale's next lower value, so that
+ * 127 scales are finite.)  A row of zeros has scale 0.  A row that holds a NaN or an infinity has scale
  * NaN and reads back as NaN.
  *
  * kda_state_quantize   -- entry i (0 <= i < n) writes state rows[i] of

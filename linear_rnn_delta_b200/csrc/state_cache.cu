@@ -166,8 +166,11 @@ __global__ void __launch_bounds__(SC_NT) state_quantize_kernel(const StateCache 
 #pragma unroll
         for (int u = 1; u < SC_UNROLL; ++u) mine = c == u ? amax[u] : mine;
         const int k = base + c * PASS + warp * RPW + sub;
-        if (c < SC_UNROLL && k < a.dk)
-            scales[k] = mine < 0x7f800000u ? __fdiv_rn(__uint_as_float(mine), TOP) : __int_as_float(0x7fc00000);
+        if (c < SC_UNROLL && k < a.dk) {
+            // a 127th of the largest finite value rounds up, and 127 times that is infinite: the scale below it there
+            const float s = fminf(__fdiv_rn(__uint_as_float(mine), TOP), FMT == FMT_INT8 ? 0x1.020406p121f : 1e38f);
+            scales[k] = mine < 0x7f800000u ? s : __int_as_float(0x7fc00000);
+        }
     }
 }
 

@@ -99,6 +99,25 @@ def test_values_on_and_next_to_the_borders(kda, fmt, amax):
 
 @gpu
 @pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+def test_rows_up_to_the_largest_value(kda, fmt):
+    """They read back finite, within a unit of the scale's last place and half a code (the smallest code of e4m3 is
+    TOP / 229376, its largest step TOP / 14)."""
+    most = torch.finfo(torch.float32).max
+    x = torch.randn(1, 1, 32, 16, generator=torch.Generator().manual_seed(5)).clamp(-1, 1) * most
+    x[0, 0, :, 3] = most
+    x[0, 0, 1, 3] = -most
+    x[0, 0, 2, 3] = torch.nextafter(torch.tensor(most), torch.tensor(0.0))
+    x[0, 0, 3] = most
+    codes, scales = cache(1, 1, 32, 16, fmt)
+    kda.kda_state_quantize(x.cuda(), codes, scales)
+    back = kda.kda_state_dequantize(codes, scales).cpu().double()
+    assert torch.isfinite(back).all() and torch.isfinite(scales).all()
+    half = most / 254 if fmt == "int8" else x.double().abs() * 2.0 ** -4 + most / 448 * 2.0 ** -10
+    assert ((back - x.double()).abs() <= half * (1 + 2.0 ** -20) + 2.0 ** -22 * x.double().abs()).all()
+
+
+@gpu
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
 def test_rows_that_are_not_finite(kda, fmt):
     x = torch.randn(2, 2, 16, 32, generator=torch.Generator().manual_seed(2))
     x[0, 0, 1, 5] = math.nan
