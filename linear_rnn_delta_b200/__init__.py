@@ -575,6 +575,12 @@ def _at(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
 
+def _written(*tensors: torch.Tensor):
+    """Tells autograd that the caller's tensors hold other values now: a backward that saved one of them (a state,
+    say) refuses to run then."""
+    torch._C._increment_version(tensors)
+
+
 def kda_linattn_chunk_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor,
                           cu_seqlens: Optional[torch.Tensor] = None, initial_state: Optional[torch.Tensor] = None,
                           final_state: Union[torch.Tensor, bool, None] = True, o: Optional[torch.Tensor] = None,
@@ -594,6 +600,7 @@ def kda_linattn_chunk_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: 
     want_states = chunk_states is not None and chunk_states is not False
     _fits_opt(initial_state, "initial_state", torch.float32, states, dev)
     sizes = (_DTYPES[dt], B, T, Hk, H, dk, dv)
+    given = [t for t in (final_state, chunk_states, o) if isinstance(t, torch.Tensor)]
     with _launching(stream, dev):
         if final_state is True:
             final_state = g.new_empty(states)
@@ -618,6 +625,8 @@ def kda_linattn_chunk_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: 
                                        ws_bytes, int(flags), _raw_stream(dev))
     if rc != 0:
         raise KdaError(rc, "kda_linattn_chunk_fwd")
+    if given:
+        _written(*given)
     if want_states:
         return o, final_state, chunk_states
     return o, final_state
@@ -696,15 +705,20 @@ def kda_linattn_decode_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g
     dt, dev, Hk, H, dk, dv, per_token = _lin_inputs(q, k, v, g, False)
     N = q.shape[0]
     _fits_opt(state, "state", torch.float32, (N, H, dk, dv), dev)
+    given = o is not None
     with _launching(stream, dev):
-        if o is None:
-            o = torch.empty_like(v)
-        else:
+        if given:
             _fits(o, "o", dt, v.shape, dev)
+        else:
+            o = torch.empty_like(v)
         rc = lib.kda_linattn_decode_step(_DTYPES[dt], N, Hk, H, dk, dv, _at(q), _at(k), _at(v), _at(g), per_token,
                                          _at(state), _at(o), int(flags), _raw_stream(dev))
     if rc != 0:
         raise KdaError(rc, "kda_linattn_decode_step")
+    if given:
+        _written(state, o)
+    else:
+        _written(state)
     return o
 
 
@@ -750,6 +764,7 @@ def kda_state_quantize(states: torch.Tensor, codes: torch.Tensor, scales: torch.
                                     _at(codes), _at(scales), _raw_stream(dev))
     if rc != 0:
         raise KdaError(rc, "kda_state_quantize")
+    _written(codes, scales)
 
 
 def kda_state_dequantize(codes: torch.Tensor, scales: torch.Tensor, slots: Optional[torch.Tensor] = None,
@@ -762,15 +777,18 @@ def kda_state_dequantize(codes: torch.Tensor, scales: torch.Tensor, slots: Optio
     _index(slots, "slots", dev)
     S, H, dk, dv = codes.shape
     n = S if slots is None else slots.numel()
+    given = out is not None
     with _launching(stream, dev):
-        if out is None:
-            out = scales.new_empty((n, H, dk, dv))
-        else:
+        if given:
             _fits(out, "out", torch.float32, (n, H, dk, dv), dev)
+        else:
+            out = scales.new_empty((n, H, dk, dv))
         rc = lib.kda_state_dequantize(fmt, n, S, H, dk, dv, _at(codes), _at(scales), _at(slots), _at(out),
                                       _raw_stream(dev))
     if rc != 0:
         raise KdaError(rc, "kda_state_dequantize")
+    if given:
+        _written(out)
     return out
 
 

@@ -229,3 +229,37 @@ def test_gradients_that_are_parts_of_others(kda, dtype):
     pad = lambda t: torch.cat([t.new_ones(1), t.flatten()])  # noqa: E731
     got = torch.autograd.grad([pad(o), pad(sf)], leaves, [pad(x["do"]), pad(x["dsf"])])
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@gpu
+@pytest.mark.parametrize("how", ["decode", "decode o", "prompt", "prompt o", "dequantize"])
+def test_a_saved_tensor_that_a_call_writes(kda, how):
+    """The backward of an earlier call refuses a state or a value that has been written since, as torch's own do."""
+    x = dev(make(45, torch.bfloat16, 1, 1, 2, 2, 64, 64, init=True))
+    one = [x[n][:, 0].contiguous() for n in "qkvg"]
+    q = x["q"].clone().requires_grad_()
+    o, _ = kda.KdaLinAttnFunction.apply(q, x["k"], x["v"], x["g"], None, x["s0"])
+    if how == "decode":
+        kda.kda_linattn_decode_step(*one, x["s0"])
+    elif how == "decode o":
+        kda.kda_linattn_decode_step(*one, x["s0"].clone(), o=x["v"][:, 0])
+    elif how == "prompt":
+        kda.kda_linattn_chunk_fwd(*(x[n] for n in "qkvg"), initial_state=x["s0"], final_state=x["s0"])
+    elif how == "prompt o":
+        kda.kda_linattn_chunk_fwd(*(x[n].clone() for n in "qkvg"), o=x["v"])
+    else:
+        codes = torch.zeros(1, 2, 64, 64, dtype=torch.int8, device="cuda")
+        kda.kda_state_dequantize(codes, torch.ones(1, 2, 64, device="cuda"), out=x["s0"])
+    with pytest.raises(RuntimeError, match="inplace"):
+        o.float().sum().backward()
+
+
+@gpu
+def test_writes_in_inference_mode(kda):
+    with torch.inference_mode():
+        x = dev(make(46, torch.float32, 1, 3, 1, 2, 32, 32, init=True))
+        o, st = kda.kda_linattn_chunk_fwd(*(x[n] for n in "qkvg"), initial_state=x["s0"], final_state=x["s0"])
+        kda.kda_linattn_decode_step(*(x[n][:, 0].contiguous() for n in "qkvg"), st)
+        codes, scales = torch.zeros(1, 2, 32, 32, dtype=torch.int8, device="cuda"), torch.zeros(1, 2, 32, device="cuda")
+        kda.kda_state_quantize(st, codes, scales)
+        assert kda.kda_state_dequantize(codes, scales, out=x["dsf"]) is x["dsf"]
