@@ -10,7 +10,7 @@ import time
 import pytest
 import torch
 
-from test_linattn import DT, check_bwd, check_fwd, dev, make
+from test_linattn import DT, TURNS, check_bwd, check_fwd, dev, make
 
 gpu = pytest.mark.gpu
 
@@ -263,3 +263,39 @@ def test_writes_in_inference_mode(kda):
         codes, scales = torch.zeros(1, 2, 32, 32, dtype=torch.int8, device="cuda"), torch.zeros(1, 2, 32, device="cuda")
         kda.kda_state_quantize(st, codes, scales)
         assert kda.kda_state_dequantize(codes, scales, out=x["dsf"]) is x["dsf"]
+
+
+# ---- which way long calls are cut ----------------------------------------------------------------------------------
+
+def up256(x):
+    return -(-x // 256) * 256
+
+
+def backward_cuts(kda, s, cu):
+    """The cuts that give the segments' share of a backward call's workspace: ("in turn" or "side by side", slots)."""
+    B, T, Hk, H, dk, dv = s.values()
+    rows, N = B * T, cu or B
+    total = int(re.search(r"(\d+) bytes", refusal(kda, s, 0, bwd=True, cu=cu)).group(1))
+    passes = 3 if dk == dv and H == Hk else 2
+    slots = N + -(-rows // 64)
+    fixed = 2 * (up256(rows * H * dk * 4) if H != Hk else 0) + 2 * up256(slots * H * dk * dv * 4) + up256(slots * H * 4)
+    cuts = set()
+    for n in range(N + 1, slots + 1):
+        states = passes * up256(n * H * dk * dv * 4)
+        if fixed + states + up256(passes * (1 + n) * H * 4) == total:
+            cuts.add(("in turn", n))
+        if fixed + states + passes * up256(n * H * 4) == total:
+            cuts.add(("side by side", n))
+    return cuts
+
+
+@pytest.mark.parametrize("i", range(len(TURNS)))
+def test_cases_in_turn_are_in_turn(kda, i):
+    """The first three of test_segments_in_turn forward, the others backward."""
+    B, T, Hk, H, dk, dv, cu, _ = TURNS[i]
+    s, N = dict(B=B, T=T, Hk=Hk, H=H, dk=dk, dv=dv), 0 if cu is None else len(cu) - 1
+    if i < 3:
+        assert "workspace" in refusal(kda, s, kda.FLAG_DEBUG_STALL, cu=N)
+    else:
+        (how, slots), = backward_cuts(kda, s, N)
+        assert how == "in turn" and slots > 2 * (N or B)
