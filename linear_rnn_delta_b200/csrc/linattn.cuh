@@ -23,7 +23,7 @@ struct LinRun {
     int g_ld;
     const float *s_in;          // [N][H] states or NULL (zero)
     float *s_out;               // state after the last step (reverse: decayed by the first token too), or NULL
-    int in_t, out_t;            // the stored state is [d_z][d_x] (transposed) instead of [d_x][d_z]
+    int in_t;                   // s_in is [d_z][d_x] (transposed) instead of [d_x][d_z]
     float *snap;                // states at boundaries every `snap_tokens` tokens, [slot][H][d_x][d_z], or NULL
     int snap_tokens;            // (reverse: the state that enters the boundary token, decayed)
     void *out;                  // [B*T][H][d_z]
@@ -33,8 +33,7 @@ struct LinRun {
     const int32_t *cu_seqlens;  // packed batch, or NULL (sequence n is rows n*T .. n*T+T-1)
     long long rows;             // tokens of the whole batch
     // token axis in segments: chunks of one (of 64 tokens, the scan's of 16; 0: not cut) and tokens, slots of all
-    // sequences, and the state
-    // that enters each slot's segment [slot][H][d_x][d_z] with the decay over it [slot][H]
+    // sequences, and the state that enters each slot's segment [slot][H][d_x][d_z] with the decay over it [slot][H]
     int seg_chunks, seg_tokens, slots;
     float *seg_state, *seg_total;
     // segments in turn (tensor-core form): tickets given out [H] and state hand-overs done [slot][H], zero at the

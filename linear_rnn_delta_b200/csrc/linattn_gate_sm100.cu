@@ -5,7 +5,7 @@
 // S_0 and G_C as the dq and dk passes left them at the chunk's ends ([d_v][d_k], fp32).
 // Four products, D in tensor memory:  Q K^T and dO V^T (bf16 operands as loaded), and S_0 dO^T, G_C V^T
 // with lanes = key channels (in which the states are contiguous) and the state in three bf16 parts (2^-24), A from
-// tensor memory.  The rest is fp32: the inner products with q and k are lane sums, 32 tokens exchanged at once.
+// tensor memory.  The rest is fp32: the inner products with q and k are lane sums, 16 tokens exchanged at once.
 // A chunk and head have 2 states (8 d_k d_v bytes) and 4 tiles to read.  What takes the time are the steps that wait for
 // one another (tiles, products, states, products): two CTAs an SM cover each other's, and 16 warps a CTA (8: 247 us)
 // shorten them.  4 x 4096 tokens, 16 heads, 128 x 128: 233 us, 2.9 TB/s.
@@ -143,7 +143,7 @@ __global__ void __launch_bounds__(NT, 2) lin_gate_kernel(const __grid_constant__
             for (int e = 0; e < DV / 16; ++e) mma_bf16_warp(tbase + TM_S, dK(d, e), dK(v, e), ID, e > 0, lead);
         }
         finish();
-        if (ok && quarter < 2) {   // row r of W, 32 columns
+        if (ok && quarter < 2) {   // row r of W, 16 columns
             const int r = quarter * 32 + lane, s0 = part_of * TW;
             float x[TW], y[TW];
             tmem_ld16(tlane + TM_D + s0, x);

@@ -7,7 +7,6 @@
 // takes small differences of large sums: with a decay of e^{-1} a token it left 2e-5 of dg (and 4e-4 of a decay's
 // own, which is a sum over tokens) where fp32 should leave 1e-7.  So the pairs are summed as they are: those
 // within a chunk one by one, the others through the states at the chunk's two ends.
-#include <mutex>
 
 #include "linattn_sm100.cuh"
 
@@ -282,7 +281,7 @@ __global__ void __launch_bounds__(GT) lin_gate_chunk_kernel(const LinGateGrad a)
     }
 }
 
-// dg of a head's own decay: the sum over its segments, in slot order and 64 bits
+// dg of a head's own decay: the sum over its chunks (slots of 64 tokens), in slot order and 64 bits
 __global__ void __launch_bounds__(128) lin_gate_head_kernel(const float *partial, int slots, int H, float *dg)
 {
     __shared__ double s_red[128];

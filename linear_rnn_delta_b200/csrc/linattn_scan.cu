@@ -22,7 +22,6 @@
 // 32 x 64: 4 and 6 us in segments of 16 tokens (of 64: 9 and 15); 2 x 1001, 8 heads, 64 x 128: 19 and 41 us.
 #include <algorithm>
 #include <cmath>
-#include <mutex>
 
 #include "linattn_sm100.cuh"
 
@@ -165,24 +164,19 @@ __global__ void __launch_bounds__(LinScanShape<DX, DZ>::NTH) lin_scan_kernel(con
             }
         }
     };
-    auto write_state = [&](float *dst, bool t, float by) {   // [DX][DZ], or transposed
+    auto write_state = [&](float *dst, float by) {   // [DX][DZ]
         if (!live) return;
 #pragma unroll
         for (int r = 0; r < 8; ++r) {
             const int i = 8 * p + r;
-            const float v[4] = {S[r][0].x * by, S[r][0].y * by, S[r][1].x * by, S[r][1].y * by};
-            if (t) {
-#pragma unroll
-                for (int c = 0; c < 4; ++c) dst[(size_t)(j + c) * DX + i] = v[c];
-            } else {
-                *reinterpret_cast<float4 *>(dst + (size_t)i * DZ + j) = make_float4(v[0], v[1], v[2], v[3]);
-            }
+            *reinterpret_cast<float4 *>(dst + (size_t)i * DZ + j) =
+                make_float4(S[r][0].x * by, S[r][0].y * by, S[r][1].x * by, S[r][1].y * by);
         }
     };
     // the state at a boundary: behind token t forward, entering it backward
     auto snap = [&](int t) {
         if (STATE || !a.snap || t < 0 || (t != len - 1 && (t + 1) % a.snap_tokens)) return;
-        write_state(a.snap + ((size_t)(n + row0 / a.snap_tokens + t / a.snap_tokens) * a.H + h) * DX * DZ, false, 1.f);
+        write_state(a.snap + ((size_t)(n + row0 / a.snap_tokens + t / a.snap_tokens) * a.H + h) * DX * DZ, 1.f);
     };
 
     if (nblk > 0) fetch(0);
@@ -278,7 +272,7 @@ __global__ void __launch_bounds__(LinScanShape<DX, DZ>::NTH) lin_scan_kernel(con
             if (t % a.snap_tokens == 0) {
                 const float g = a.g[((size_t)row0 + t) * a.g_ld + h];
                 const float by = g != g ? g : fix_exp2(fix_log2(fminf(fmaxf(g, -1e4f), 1e4f)));
-                write_state(a.snap + ((size_t)(n + row0 / a.snap_tokens + (t - 1) / a.snap_tokens) * a.H + h) * DX * DZ, false, by);
+                write_state(a.snap + ((size_t)(n + row0 / a.snap_tokens + (t - 1) / a.snap_tokens) * a.H + h) * DX * DZ, by);
             }
         }
     }
@@ -289,7 +283,7 @@ __global__ void __launch_bounds__(LinScanShape<DX, DZ>::NTH) lin_scan_kernel(con
         by = g != g ? g : fix_exp2(fix_log2(fminf(fmaxf(g, -1e4f), 1e4f)));
     }
     if (STATE) {
-        write_state(a.seg_state + woff, false, by);
+        write_state(a.seg_state + woff, by);
         if (cblk == 0 && tid < 32) {
             if (rev && tid == 0) {   // the steps had the decays of the tokens behind theirs: this one is still to come
                 const float g = a.g[((size_t)row0 + beg) * a.g_ld + h];
@@ -302,7 +296,7 @@ __global__ void __launch_bounds__(LinScanShape<DX, DZ>::NTH) lin_scan_kernel(con
             if (tid == 0) a.seg_total[(size_t)work.slot * a.H + h] = any_nan ? NAN : fix_exp2(sum);
         }
     } else if (a.s_out && closing) {
-        write_state(a.s_out + soff, a.out_t != 0, by);
+        write_state(a.s_out + soff, by);
     }
 }
 
