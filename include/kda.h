@@ -91,8 +91,9 @@ enum kda_status {
     KDA_ERR_UNSUPPORTED = 2,   /* valid but not implemented (head dims, chunk size) */
     KDA_ERR_RANGE = 3,         /* a gate outside the declared range (KDA_FLAG_VALIDATE_RANGE) */
     KDA_ERR_CUDA = 4,          /* a CUDA runtime call or launch failed */
-    KDA_ERR_DEVICE_TIMEOUT = 5 /* kda_device_status: a kernel gave up a bounded wait or found
-                                  a chunk's operands missing; the affected outputs are undefined */
+    KDA_ERR_DEVICE_TIMEOUT = 5 /* kda_device_status: a kernel recorded a failure, its bits say
+                                  which (a bounded wait given up, a chunk's operands missing: the
+                                  affected outputs are undefined; an index out of range) */
 };
 
 /* Flags. */
@@ -103,7 +104,8 @@ enum kda_status {
  * synchronises `stream`.  A violation returns KDA_ERR_RANGE (gates) or
  * KDA_ERR_INVALID_ARG (cu_seqlens) and launches nothing.  With
  * KDA_FLAG_GATE_LOGITS only cu_seqlens is checked (logits have no range).
- * Accepted by kda_chunk_fwd, kda_chunk_fwd_ws and kda_decode_step.  Without
+ * Accepted by kda_chunk_fwd, kda_chunk_fwd_ws, kda_decode_step,
+ * kda_linattn_chunk_fwd and kda_linattn_decode_step.  Without
  * it no device value is checked: the kernels compute out-of-range gates as
  * the recurrence defines them, and a cu_seqlens that breaks its contract
  * makes them read and write out of bounds. */
@@ -364,7 +366,8 @@ int kda_decode_step(int variant, int gate_range, int dtype,
  *            h / (H / Hk)
  *   g      : fp32 log-decays, [B,T,H] (g_per_token != 0) or [H], one for each
  *            head (g_per_token = 0).  Contract: g <= 0; -infinity is a decay
- *            of 0 (nothing of the state is kept).  Not checked unless
+ *            of 0 (nothing finite of the state is kept; 0 times an infinity
+ *            or a NaN in it is NaN).  Not checked unless
  *            KDA_FLAG_VALIDATE_RANGE asks for it.  g and dg need 4-byte
  *            alignment only.
  *   states : fp32 [N,H,d_k,d_v]
@@ -405,14 +408,22 @@ int kda_linattn_chunk_fwd(int dtype, int B, int T, int Hk, int H, int d_k, int d
  * (the inputs' dtype) and dL/dS_final = d_final_state (NULL = 0): dq, dk, dv
  * in the inputs' dtype and layouts (dq and dk summed over the value heads that
  * share them), dg fp32 in g's layout (summed over all tokens for g of [H]),
- * d_initial_state fp32 (NULL: not written).  Each is formed in fp32 and
- * rounded once.  With G_t = dL/dS_t,
+ * d_initial_state fp32 (NULL: not written).  Sums are held in fp32 and rounded
+ * once; the token scan rounds nothing else to fewer bits.  The tensor-core
+ * form does, in the forward's o and in dq, dk and dv alike: each decayed weight
+ * of a pair of tokens of one chunk to bf16 (off by 2^-8 of it at most), a
+ * state's part in them to 2^-16, and in a chunk that decays below 2^-96 the
+ * decayed query to bf16.  States, dg and d_initial_state keep 2^-24.
+ * With G_t = dL/dS_t,
  *   dq_t = S_t d_o_t,  dk_t = G_t v_t,  dv_t = G_t^T k_t,
  *   G_t = a_{t+1} G_{t+1} + q_t d_o_t^T,
  *   dg_t = sum_{r >= t} (q_r . dq_r - k_r . dk_r) + <S_T, dL/dS_T>.
  * At g_t = -infinity dg_t is 0, the slope of e^g there.  Deterministic.  No
  * output may share memory with an input.  workspace as above,
- * kda_linattn_chunk_bwd_workspace_size bytes.  Flags: KDA_FLAG_FORCE_SCAN,
+ * kda_linattn_chunk_bwd_workspace_size bytes: two fp32 states for every 64
+ * tokens of a sequence and head (2 KB for each token and head at 128 x 128,
+ * twice the bf16 q, k, v and o together), the fp32 dq and dk of every value
+ * head where heads share keys, and the segments' states.  Flags: KDA_FLAG_FORCE_SCAN,
  * KDA_FLAG_DEBUG_STALL.
  */
 size_t kda_linattn_chunk_bwd_workspace_size(int dtype, int B, int T, int Hk, int H, int d_k, int d_v,
@@ -450,7 +461,9 @@ int kda_linattn_decode_step(int dtype, int N, int Hk, int H, int d_k, int d_v,
  *   `states` [num_states,H,d_k,d_v] to slot slots[i].  rows, slots: int32
  *   DEVICE arrays of n entries, NULL = 0 .. n-1.  An entry with a negative row
  *   or slot is skipped; where several entries name one slot, the last one is
- *   written.  Slots that no entry names are left as they are.
+ *   written (each entry looks through those behind it, so that the time of
+ *   calls with slots has a part that grows with n^2 H: nothing at some hundred
+ *   entries, most of it at 10^5 small states).  Slots that no entry names are left as they are.
  * kda_state_dequantize -- states[i] = slot slots[i], for `states`
  *   [n,H,d_k,d_v]; a negative slot gives zeros (an empty state).
  * An index that is too large is never followed: the entry is skipped (written

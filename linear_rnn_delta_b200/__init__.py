@@ -641,7 +641,9 @@ def kda_linattn_chunk_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: 
     d_final_state (fp32 or None for zero).  Returns (dq, dk, dv, dg,
     d_initial_state): dq, dk, dv in the inputs' dtype (dq and dk summed over
     the value heads that share them), dg fp32 shaped like g, d_initial_state
-    fp32 (None unless ``d_initial_state``)."""
+    fp32 (None unless ``d_initial_state``).  The workspace, from torch's
+    caching allocator, is two fp32 states for every 64 tokens and head (2 KB
+    for each token and head at 128 x 128)."""
     dt, dev, Hk, H, dk, dv, per_token = _lin_inputs(q, k, v, g, True)
     B, T = q.shape[:2]
     _fits_opt(d_o, "d_o", dt, v.shape, dev)
@@ -745,7 +747,8 @@ def kda_state_quantize(states: torch.Tensor, codes: torch.Tensor, scales: torch.
     states [M,H,d_k,d_v]; codes [S,H,d_k,d_v] int8 or float8_e4m3fn; scales
     fp32 [S,H,d_k].  Entry i writes state ``rows[i]`` (i without rows) to slot
     ``slots[i]`` (i without slots); int32 tensors of one length.  Negative
-    entries are skipped; of several entries for one slot the last is written."""
+    entries are skipped; of several entries for one slot the last is written
+    (found by looking through the entries: meant for calls of some thousand)."""
     if states.dim() != 4:
         raise ValueError("states must be [M,H,d_k,d_v]")
     dev = states.device
@@ -829,7 +832,8 @@ def kda_device_status(stream=None, device=None):
     """(status code, failure bits) of the library's kernels on the current
     device since the previous query (C: kda_device_status): waits for
     ``stream``, then reads and clears the word.  Code 0 = no failure, 5 =
-    KDA_ERR_DEVICE_TIMEOUT (bits DEVICE_WAIT_TIMEOUT, DEVICE_SLOT_MISSING)."""
+    KDA_ERR_DEVICE_TIMEOUT (bits DEVICE_WAIT_TIMEOUT, DEVICE_SLOT_MISSING, and
+    DEVICE_BAD_INDEX for a state-cache index that was too large)."""
     dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
     bits = ctypes.c_uint(0)
     rc = lib.kda_device_status(_stream(stream, dev), ctypes.byref(bits))

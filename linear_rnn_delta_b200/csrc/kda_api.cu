@@ -664,7 +664,7 @@ extern "C" const char *kda_error_string(int code)
     case KDA_ERR_RANGE: return "KDA_ERR_RANGE: gate outside the declared range";
     case KDA_ERR_CUDA: return "KDA_ERR_CUDA: CUDA runtime or launch failure";
     case KDA_ERR_DEVICE_TIMEOUT:
-        return "KDA_ERR_DEVICE_TIMEOUT: a kernel gave up a bounded wait or found its input missing";
+        return "KDA_ERR_DEVICE_TIMEOUT: a kernel gave up a bounded wait, or found its input missing or an index out of range";
     }
     return "unknown kda status code";
 }
