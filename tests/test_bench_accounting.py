@@ -72,6 +72,17 @@ def test_traffic_table_is_consistent():
             assert abs(sum(e["per_kernel"].values()) - e["dram_bytes_per_launch"]) <= 1, name
 
 
+def test_traffic_belongs_to_the_present_sources():
+    """Otherwise the bench reports none: captures are taken anew when their kernels' sources change."""
+    for name, sources in (("chunk_fwd_ckda_8x16x8192_split", bench.CHUNK_SOURCES),
+                          ("chunk_fwd_kda_4x16x4096_split", bench.CHUNK_SOURCES),
+                          ("chunk_fwd_rda_varlen_split", bench.CHUNK_SOURCES),
+                          ("chunk_fwd_gdn2_varlen_split", bench.CHUNK_SOURCES),
+                          ("decode_ckda_256x32", bench.DECODE_SOURCES),
+                          ("backward_kda_4x16x4096", bench.BWD_SOURCES)):
+        assert bench.measured_traffic(name, sources).get("dram_bytes_per_launch", 0) > 0, name
+
+
 def test_traffic_is_dropped_when_the_sources_change(monkeypatch):
     name = "chunk_fwd_ckda_8x16x8192_split"
     monkeypatch.setattr(bench, "source_digest", lambda paths: "0" * 64)
