@@ -18,8 +18,11 @@ constexpr int C = 64;                                 // tokens of a chunk
 constexpr uint32_t TILE = 16384;                      // [64 tokens][128 channels] bf16: two panels of 64 channels
 constexpr uint32_t STAGE = 3 * TILE;                  // X, Y, Z
 
-constexpr long long WAIT_LIMIT = 1ll << 32;           // cycles, about 2 s (the last waits of a CTA)
-constexpr uint32_t WAIT_NS = 1000000, WAIT_POLLS = 2000;   // a poll sleeps for up to 1 ms: about 2 s
+constexpr long long WAIT_LIMIT = 1ll << 32;           // cycles, about 2 s (hand-overs and the last waits of a CTA)
+// Polls that sleep for 4 us: about 2 s.  (Given more time, a poll was measured to sleep 4 us all the same, and a limit
+// of 2000 polls of 1 ms to be over after 8 ms: less than a CTA may wait for the segments before its own.  Reading a
+// timer between polls made the walks 1 to 2 % longer.)
+constexpr uint32_t WAIT_NS = 4000, WAIT_POLLS = 500000;
 constexpr long long STALL_LIMIT = 1ll << 21;          // testing aid: about 1 ms
 constexpr unsigned DEV_WAIT_TIMEOUT = 1u;
 

@@ -299,3 +299,28 @@ def test_cases_in_turn_are_in_turn(kda, i):
     else:
         (how, slots), = backward_cuts(kda, s, N)
         assert how == "in turn" and slots > 2 * (N or B)
+
+
+# ---- long waits ----------------------------------------------------------------------------------------------------
+
+LONG_DOC = dict(B=1, T=600000, Hk=1, H=12, dk=64, dv=64)   # 32 documents, all but one of them short
+
+
+def test_a_long_document_is_walked_in_turn(kda):
+    assert "workspace" in refusal(kda, LONG_DOC, kda.FLAG_DEBUG_STALL, cu=32)
+
+
+@gpu
+def test_last_segment_waits_for_a_long_document(kda):
+    """Its CTAs all start at once; the last waits for the whole walk before it, some 20 ms.  Every token resets, as
+    in test_resets_all_along_a_long_segment."""
+    T, H, d = LONG_DOC["T"], LONG_DOC["H"], LONG_DOC["dk"]
+    cu = torch.cat([torch.arange(0, 31 * 30, 30), torch.tensor([31 * 30, T])]).to(torch.int32).cuda()
+    q, k, v = small_ints(1, T, 1, d, seed=1), small_ints(1, T, 1, d, seed=2), small_ints(1, T, H, d, seed=3)
+    g = torch.full((H,), -math.inf, device="cuda")
+    kda.kda_device_status()
+    o, sf = kda.kda_linattn_chunk_fwd(q, k, v, g, cu_seqlens=cu)
+    assert kda.kda_device_status() == (0, 0)
+    assert torch.equal(o.float(), (q.float() * k.float()).sum(-1, keepdim=True) * v.float())
+    ends = cu[1:].long() - 1
+    assert torch.equal(sf, k[0, ends].float()[..., None] * v[0, ends].float()[:, :, None, :])
