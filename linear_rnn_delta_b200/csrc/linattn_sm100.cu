@@ -870,7 +870,7 @@ LinCut lin_cut(int num_seqs, int T, int H, int passes, long long rows, bool pack
     for (int seg = 4; seg < longest; seg += 1 + seg / 16) {
         const double count = units * (packed ? 1 / (1 - std::exp(-seg / mean)) : std::ceil(mean / seg));
         for (int turns = 0; turns < 2; ++turns) {
-            if (turns && packed && num_seqs > TURN_SEQS) break;
+            if (turns && ((packed && num_seqs > TURN_SEQS) || (packed ? rows : T) > TURN_ROWS)) break;
             const double rate = turns ? 1 : 1.7, start = turns ? 6 : 16, walk = rate * seg + start;
             double cut = std::max(walk, (rate * all + start * count) / S + 0.5 * walk);
             if (!packed) cut = turns ? std::max(cut, std::ceil(count / S) * walk) : std::ceil(count / S) * walk;

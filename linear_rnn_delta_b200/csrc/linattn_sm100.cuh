@@ -58,6 +58,9 @@ template <int U = C> __device__ __forceinline__ Work lin_work(const LinRun &a, i
 // sequence's earlier ones come before its later ones, so that the one that hands over a state is running or done
 // already.  `scratch` holds 2 * 32 words.  A slot of -1: no segment is left.
 constexpr int TURN_SEQS = 896;   // packed sequences at most: one to a thread
+// A sequence's tokens at most: its last segment may wait for the walk of all others, 2.2 us a chunk of 128 x 128, 5.5
+// with a reset and a NaN in each (0.29 to 0.72 s in all, where a wait gives up after 2).
+constexpr int TURN_ROWS = 1 << 23;
 __device__ __forceinline__ Work lin_turn(const LinRun &a, int h, int *scratch)
 {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;

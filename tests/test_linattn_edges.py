@@ -310,6 +310,13 @@ def test_a_long_document_is_walked_in_turn(kda):
     assert "workspace" in refusal(kda, LONG_DOC, kda.FLAG_DEBUG_STALL, cu=32)
 
 
+def test_no_walk_is_waited_for_longer_than_a_wait_lasts(kda):
+    """5.5 us a chunk at the slowest measured: 2^23 tokens are 0.7 s of the 2 s after which a wait gives up."""
+    for s, cu in ((LONG_DOC, 32), (STALLED, 0)):
+        assert "workspace" in refusal(kda, dict(s, T=1 << 23), kda.FLAG_DEBUG_STALL, cu=cu)
+        assert "in turn" in refusal(kda, dict(s, T=(1 << 23) + 1), kda.FLAG_DEBUG_STALL, cu=cu)
+
+
 @gpu
 def test_last_segment_waits_for_a_long_document(kda):
     """Its CTAs all start at once; the last waits for the whole walk before it, some 20 ms.  Every token resets, as
