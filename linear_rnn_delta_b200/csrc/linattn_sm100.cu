@@ -858,6 +858,8 @@ LinCut lin_cut(int num_seqs, int T, int H, int passes, long long rows, bool pack
     // (side by side 261), 12x4096 283 and 222 (in turn), 10x8192 543 and 386 (in turn), backward of 4x4096 670 and 595
     // (in turn); packed, 30 sequences of 65536 tokens, 4 heads, 246 and 186 (side by side); 7 of 16384 whole 129
     // (in turn 140); 16 of 32768, 32 heads, 427 and 359 (in turn).
+    // A B200's SMs: a constant, so that the workspace's size follows from the call's sizes alone.  The costs were measured
+    // at 128 x 128 and serve the smaller head sizes, too, whose chunks take 15 % less.
     const int S = 148;
     const double units = (double)num_seqs * H * passes;
     const double mean = packed ? std::max(1.0, (double)rows / C / num_seqs) : (double)((T + C - 1) / C);
