@@ -549,11 +549,28 @@ def _launching(stream, dev):
     that the kernels run on (what torch hands out is then free on that stream)."""
     if stream is None:
         return _HERE if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+    return torch.cuda.stream(_given_stream(stream, dev))
+
+
+def _given_stream(stream, dev):
     if not hasattr(stream, "cuda_stream"):
         stream = torch.cuda.ExternalStream(int(stream), dev)
     if stream.device != dev:
         raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
-    return torch.cuda.stream(stream)
+    return stream
+
+
+def _used_on(stream, dev, *tensors: Optional[torch.Tensor]):
+    """Behind a call on a given stream: its tensors' memory is not handed out again before the work that the stream, and
+    the current one, have by the time they are dropped."""
+    if stream is None:
+        return
+    stream, here = _given_stream(stream, dev), torch.cuda.current_stream(dev)
+    if stream.cuda_stream != here.cuda_stream:
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+                t.record_stream(here)
 
 
 @functools.lru_cache(maxsize=256)
@@ -627,6 +644,7 @@ def kda_linattn_chunk_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: 
         raise KdaError(rc, "kda_linattn_chunk_fwd")
     if given:
         _written(*given)
+    _used_on(stream, dev, q, k, v, g, cu_seqlens, initial_state, final_state, chunk_states, o)
     if want_states:
         return o, final_state, chunk_states
     return o, final_state
@@ -664,6 +682,7 @@ def kda_linattn_chunk_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: 
                                        _raw_stream(dev))
     if rc != 0:
         raise KdaError(rc, "kda_linattn_chunk_bwd")
+    _used_on(stream, dev, q, k, v, g, d_o, d_final_state, cu_seqlens, initial_state, dqt, dkt, dvt, dgt, ds0)
     return dqt, dkt, dvt, dgt, ds0
 
 
@@ -721,6 +740,7 @@ def kda_linattn_decode_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g
         _written(state, o)
     else:
         _written(state)
+    _used_on(stream, dev, q, k, v, g, state, o)
     return o
 
 
@@ -768,6 +788,7 @@ def kda_state_quantize(states: torch.Tensor, codes: torch.Tensor, scales: torch.
     if rc != 0:
         raise KdaError(rc, "kda_state_quantize")
     _written(codes, scales)
+    _used_on(stream, dev, states, codes, scales, slots, rows)
 
 
 def kda_state_dequantize(codes: torch.Tensor, scales: torch.Tensor, slots: Optional[torch.Tensor] = None,
@@ -792,6 +813,7 @@ def kda_state_dequantize(codes: torch.Tensor, scales: torch.Tensor, slots: Optio
         raise KdaError(rc, "kda_state_dequantize")
     if given:
         _written(out)
+    _used_on(stream, dev, codes, scales, slots, out)
     return out
 
 

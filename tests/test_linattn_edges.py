@@ -331,3 +331,76 @@ def test_last_segment_waits_for_a_long_document(kda):
     assert torch.equal(o.float(), (q.float() * k.float()).sum(-1, keepdim=True) * v.float())
     ends = cu[1:].long() - 1
     assert torch.equal(sf, k[0, ends].float()[..., None] * v[0, ends].float()[:, :, None, :])
+
+
+# ---- streams -------------------------------------------------------------------------------------------------------
+
+CALLS = {
+    "prompt": lambda kda, x, s: kda.kda_linattn_chunk_fwd(x["q"], x["k"], x["v"], x["g"], initial_state=x["s0"], stream=s),
+    "backward": lambda kda, x, s: kda.kda_linattn_chunk_bwd(x["q"], x["k"], x["v"], x["g"], x["do"], x["dsf"],
+                                                            initial_state=x["s0"], stream=s),
+    "decode": lambda kda, x, s: (kda.kda_linattn_decode_step(x["q1"], x["k1"], x["v1"], x["g1"], x["s0"], stream=s),),
+    "dequantize": lambda kda, x, s: (kda.kda_state_dequantize(x["codes"], x["scales"], x["slots"], stream=s),),
+}
+
+
+def stream_inputs():
+    x = dev(make(47, torch.bfloat16, 2, 200, 1, 2, 64, 64, init=True))
+    x.update({n + "1": x[n][:, 0].contiguous() for n in "qkvg"})
+    x["codes"] = torch.randint(-127, 128, (4, 2, 64, 64), dtype=torch.int8, device="cuda")
+    x["scales"], x["slots"] = torch.rand(4, 2, 64, device="cuda"), torch.tensor([2, 0, 3], dtype=torch.int32, device="cuda")
+    return x
+
+
+@gpu
+@pytest.mark.parametrize("name", CALLS)
+@pytest.mark.parametrize("raw", [False, True])
+def test_tensors_dropped_behind_a_call_on_another_stream(kda, name, raw):
+    """Inputs that are dropped while the given stream has yet to come to the call, and outputs that are dropped while
+    the current stream has yet to read them, keep their memory until then."""
+    x = stream_inputs()
+    copy = lambda: {n: t.clone() for n, t in x.items() if t is not None}  # noqa: E731
+    want = [t.clone() for t in CALLS[name](kda, copy(), None) if t is not None]
+    side = torch.cuda.Stream()
+    s = side.cuda_stream if raw else side
+    torch.cuda.synchronize()
+
+    y = copy()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(50_000_000)   # some 25 ms
+    got = [t for t in CALLS[name](kda, y, s) if t is not None]
+    sizes = {t.numel() * t.element_size() for t in y.values()}
+    del y
+    junk = [torch.full((n,), 0x7f, dtype=torch.uint8, device="cuda") for n in sizes for _ in range(12)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want)), "inputs"
+    del junk, got
+
+    y = copy()
+    side.wait_stream(torch.cuda.current_stream())
+    got = [t for t in CALLS[name](kda, y, s) if t is not None]
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda._sleep(50_000_000)
+    read = [t.clone() for t in got]
+    sizes = {t.numel() * t.element_size() for t in got}
+    del got
+    with torch.cuda.stream(side):
+        junk = [torch.full((n,), 0x7f, dtype=torch.uint8, device="cuda") for n in sizes for _ in range(12)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(read, want)), "outputs"
+    del junk
+
+
+@gpu
+def test_captured_on_a_given_stream(kda):
+    x = stream_inputs()
+    want = [t.clone() for t in CALLS["prompt"](kda, x, None)]
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        side.wait_stream(torch.cuda.current_stream())
+        got = CALLS["prompt"](kda, x, side)
+        torch.cuda.current_stream().wait_stream(side)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
