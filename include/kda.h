@@ -381,11 +381,11 @@ int kda_decode_step(int variant, int gate_range, int dtype,
  * may be lost.
  * Flags: KDA_FLAG_VALIDATE_RANGE (g and cu_seqlens; waits for the outcome),
  * KDA_FLAG_FORCE_SCAN (token-by-token kernel) and KDA_FLAG_DEBUG_STALL.  After
- * KDA_DEVICE_WAIT_TIMEOUT (kda_device_status) the final state of the affected
- * (sequence, head) is NaN and its o and chunk_states are undefined, as are the
- * gradients of a backward call, except for dg of a chunk whose own wait ran
- * out, which is NaN.  o does not depend on tokens
- * behind it nor on other sequences of the batch, whatever their values.
+ * KDA_DEVICE_WAIT_TIMEOUT (kda_device_status) the outputs of the affected
+ * (sequence, head) are undefined, those of a backward call all; a state that
+ * the kernel that gave up had yet to write, and dg of a chunk whose own wait
+ * ran out, are NaN.  o does not depend on tokens behind it nor on other
+ * sequences of the batch, whatever their values.
  */
 
 /*
@@ -423,8 +423,8 @@ int kda_linattn_chunk_fwd(int dtype, int B, int T, int Hk, int H, int d_k, int d
  * kda_linattn_chunk_bwd_workspace_size bytes: two fp32 states for every 64
  * tokens of a sequence and head (2 KB for each token and head at 128 x 128,
  * twice the bf16 q, k, v and o together), the fp32 dq and dk of every value
- * head where heads share keys, and the segments' states.  Flags: KDA_FLAG_FORCE_SCAN,
- * KDA_FLAG_DEBUG_STALL.
+ * head where heads share keys, and the segments' states.  Flags:
+ * KDA_FLAG_FORCE_SCAN, KDA_FLAG_DEBUG_STALL.
  */
 size_t kda_linattn_chunk_bwd_workspace_size(int dtype, int B, int T, int Hk, int H, int d_k, int d_v,
                                             int has_cu_seqlens, int num_seqs);
@@ -454,8 +454,8 @@ int kda_linattn_decode_step(int dtype, int N, int Hk, int H, int d_k, int d_v,
  * (int8) or 448 (e4m3); code = the nearest to x TOP / A, ties to the even
  * code, decided as in exact arithmetic; the value read back is code * scale.
  * (int8, A = the largest finite value: the scale's next lower value, so that
- * 127 scales are finite.)  A row of zeros has scale 0.  A row that holds a NaN or an infinity has scale
- * NaN and reads back as NaN.
+ * 127 scales are finite.)  A row of zeros has scale 0.  A row that holds a NaN
+ * or an infinity has scale NaN and reads back as NaN.
  *
  * kda_state_quantize   -- entry i (0 <= i < n) writes state rows[i] of
  *   `states` [num_states,H,d_k,d_v] to slot slots[i].  rows, slots: int32
@@ -463,7 +463,8 @@ int kda_linattn_decode_step(int dtype, int N, int Hk, int H, int d_k, int d_v,
  *   or slot is skipped; where several entries name one slot, the last one is
  *   written (each entry looks through those behind it, so that the time of
  *   calls with slots has a part that grows with n^2 H: nothing at some hundred
- *   entries, most of it at 10^5 small states).  Slots that no entry names are left as they are.
+ *   entries, most of it at 10^5 small states).  Slots that no entry names are
+ *   left as they are.
  * kda_state_dequantize -- states[i] = slot slots[i], for `states`
  *   [n,H,d_k,d_v]; a negative slot gives zeros (an empty state).
  * An index that is too large is never followed: the entry is skipped (written
