@@ -413,8 +413,8 @@ int kda_linattn_chunk_fwd(int dtype, int B, int T, int Hk, int H, int d_k, int d
  * form does, in the forward's o and in dq, dk and dv alike: each decayed weight
  * of a pair of tokens of one chunk to bf16 (off by 2^-8 of it at most), a
  * state's part in them to 2^-16, and in a chunk that decays below 2^-96 the
- * decayed query to bf16.  What goes into states, dg and d_initial_state is off
- * by 2^-24 at most before the tensor cores' fp32 sums.  With G_t = dL/dS_t,
+ * decayed query to bf16.  What goes into the fp32 sums of states, dg and
+ * d_initial_state is off by 2^-24 (values) and 2^-22 (exponentials).  With G_t = dL/dS_t,
  *   dq_t = S_t d_o_t,  dk_t = G_t v_t,  dv_t = G_t^T k_t,
  *   G_t = a_{t+1} G_{t+1} + q_t d_o_t^T,
  *   dg_t = sum_{r >= t} (q_r . dq_r - k_r . dk_r) + <S_T, dL/dS_T>.
